@@ -31,6 +31,23 @@ _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _f = ctypes.c_float
 
+CACHE_F16, CACHE_E4M3 = 0, 1
+ROPE_KINDS = {"linear": 1, "ntk": 2, "bands": 3, "ramp": 4}
+
+
+class PagedCacheDesc(ctypes.Structure):
+    """tri_paged_cache."""
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("table", _p),
+                ("pages", _i64), ("page_size", _i64), ("page_stride", _i64), ("heads", _i64), ("head_dim", _i64),
+                ("seqs", _i64), ("seq_pages", _i64), ("table_stride", _i64), ("dtype", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    """tri_rope_scaling."""
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("context", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
 SIGNATURES = {
     "tri_status_string": (ctypes.c_char_p, [_i]),
     "tri_version": (_i, []),
@@ -57,6 +74,13 @@ SIGNATURES = {
     "tri_qknorm_rope": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _f, _p]),
     "tri_attention_decode_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "tri_attention_decode": (_i, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _p, _sz, _p]),
+    "tri_rope_table_scaled": (_i, [_p, _i64, _i64, ctypes.c_double, ctypes.POINTER(RopeScaling), _p]),
+    "tri_paged_qknorm_rope": (_i, [_p, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i, _p, _i64,
+                                   ctypes.POINTER(PagedCacheDesc), _i64, _i64, _f, _p]),
+    "tri_paged_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "tri_paged_attention": (_i, [_p, _i64, _p, _p, ctypes.POINTER(PagedCacheDesc), _p, _i64, _i64, _i64, _f, _p, _sz,
+                                 _p]),
+    "tri_copy_pages": (_i, [_p, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _p]),
 }
 
 

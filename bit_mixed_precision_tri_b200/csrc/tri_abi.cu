@@ -97,6 +97,31 @@ tri_status attn_shape(int64_t M, int64_t H, int64_t Hkv, int64_t Lmax, int64_t m
   return TRI_OK;
 }
 
+// a paged cache that the kernels can address: every product below fits in 64
+// bits, every index of a page or a table entry in 31
+tri_status check_cache(const tri_paged_cache* c) {
+  if (!c || !c->k || !c->v || !c->table) return TRI_ERR_INVALID_ARG;
+  if (c->dtype != TRI_CACHE_F16 && c->dtype != TRI_CACHE_E4M3) return TRI_ERR_INVALID_ARG;
+  if (c->dtype == TRI_CACHE_E4M3 && (!c->k_scale || !c->v_scale)) return TRI_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return TRI_ERR_SHAPE;
+  if (c->page_size < 8 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return TRI_ERR_SHAPE;
+  if (c->heads < 1 || c->heads > 65535 || c->pages < 1 || c->pages > kMaxDim) return TRI_ERR_SHAPE;
+  if (c->page_stride < c->heads * c->page_size * c->head_dim || c->page_stride % c->head_dim != 0 ||
+      c->page_stride > (int64_t(1) << 38))
+    return TRI_ERR_SHAPE;
+  if (c->seqs < 1 || c->seqs > kMaxDim || c->seq_pages < 1 || c->table_stride < 0 || c->table_stride > kMaxDim)
+    return TRI_ERR_SHAPE;
+  if (c->seq_pages > (int64_t(1) << 30) / c->page_size) return TRI_ERR_SHAPE;   // positions stay below 2^30
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->table, 4) || !aligned(c->k_scale, 4) ||
+      !aligned(c->v_scale, 4))
+    return TRI_ERR_ALIGNMENT;
+  return TRI_OK;
+}
+
+bool row_stride_ok(int64_t stride, int64_t width, int64_t rows) {
+  return stride % 8 == 0 && stride >= 0 && stride <= (int64_t(1) << 31) && (rows == 1 || stride >= width);
+}
+
 int auto_path(int fmt, int64_t M, int64_t N, int64_t K) {
   if (M <= 16 && path_supported(fmt, TRI_PATH_I8, M, N, K)) return TRI_PATH_I8;
   if (M <= 16 && path_supported(fmt, TRI_PATH_MMA, M, N, K)) return TRI_PATH_MMA;
@@ -471,6 +496,106 @@ tri_status tri_attention_decode(const uint16_t* q, const uint16_t* kcache, const
       reinterpret_cast<const __half*>(q), reinterpret_cast<const __half*>(kcache),
       reinterpret_cast<const __half*>(vcache), pos, reinterpret_cast<__half*>(out), M, H, Hkv, Lmax, max_len,
       workspace, di.sms, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- paged cache
+tri_status tri_rope_table_scaled(float* cs, int64_t Lmax, int64_t rot, double theta, const tri_rope_scaling* scaling,
+                                 void* stream) {
+  if (!cs || !(theta > 1.0) || !(theta < 1e300)) return TRI_ERR_INVALID_ARG;
+  if (scaling) {
+    if (scaling->kind < TRI_ROPE_LINEAR || scaling->kind > TRI_ROPE_RAMP) return TRI_ERR_INVALID_ARG;
+    if (!(scaling->factor >= 1.0) || !(scaling->factor < 1e30)) return TRI_ERR_INVALID_ARG;
+    if (scaling->kind >= TRI_ROPE_BANDS &&
+        (!(scaling->context > 0.0) || !(scaling->context < 1e30) || !(scaling->low > 0.0) ||
+         !(scaling->high > scaling->low) || !(scaling->high < 1e30)))
+      return TRI_ERR_INVALID_ARG;
+  }
+  if (rot < 16 || rot > 128 || rot % 16 != 0 || Lmax < 1 || Lmax > (int64_t(1) << 24)) return TRI_ERR_SHAPE;
+  if (!aligned(cs, 16)) return TRI_ERR_ALIGNMENT;
+  DevInfo di;
+  tri_status st = device_info(&di);
+  if (st != TRI_OK) return st;
+  return from_cuda(tri::launch_rope_table_scaled(reinterpret_cast<float2*>(cs), Lmax, rot, theta, scaling,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+tri_status tri_paged_qknorm_rope(const uint16_t* qkv, int64_t qkv_stride, const int32_t* pos, const int32_t* seq,
+                                 const uint16_t* gq, const uint16_t* gk, const float* cs, int64_t cs_rows,
+                                 int64_t rot, int interleaved, uint16_t* q_out, int64_t q_stride,
+                                 const tri_paged_cache* cache, int64_t T, int64_t H, float eps, void* stream) {
+  if (!qkv || !pos || !cs || !q_out || (!gq) != (!gk)) return TRI_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !(eps < 1e30f)) return TRI_ERR_INVALID_ARG;
+  tri_status st = check_cache(cache);
+  if (st != TRI_OK) return st;
+  const int64_t dh = cache->head_dim, Hkv = cache->heads;
+  if (T < 1 || T > kMaxDim || H < 1 || H > 65535 || H % Hkv != 0) return TRI_ERR_SHAPE;
+  if (rot < 16 || rot > dh || rot % 16 != 0 || cs_rows < 1 || cs_rows > (int64_t(1) << 24)) return TRI_ERR_SHAPE;
+  if (!row_stride_ok(qkv_stride, (H + 2 * Hkv) * dh, T) || !row_stride_ok(q_stride, H * dh, T)) return TRI_ERR_SHAPE;
+  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(cs, 16) || !aligned(gq, 16) || !aligned(gk, 16) ||
+      !aligned(pos, 4) || !aligned(seq, 4))
+    return TRI_ERR_ALIGNMENT;
+  DevInfo di;
+  if ((st = device_info(&di)) != TRI_OK) return st;
+  return from_cuda(tri::launch_paged_qknorm_rope(
+      reinterpret_cast<const __half*>(qkv), qkv_stride, pos, seq, reinterpret_cast<const __half*>(gq),
+      reinterpret_cast<const __half*>(gk), cs, cs_rows, rot, interleaved != 0, reinterpret_cast<__half*>(q_out),
+      q_stride, *cache, T, H, eps, di.sms, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+tri_status paged_attn_shape(int64_t M, int64_t H, int64_t heads, int64_t head_dim) {
+  if (head_dim != 64 && head_dim != 128) return TRI_ERR_SHAPE;
+  if (M < 1 || M > (int64_t(1) << 24) || heads < 1 || heads > 65535 || H < 1 || H % heads != 0 || H / heads > 16)
+    return TRI_ERR_SHAPE;
+  return M * H > kMaxDim ? TRI_ERR_SHAPE : TRI_OK;
+}
+}  // namespace
+
+size_t tri_paged_attention_workspace_bytes(int64_t M, int64_t H, int64_t heads, int64_t head_dim) {
+  if (paged_attn_shape(M, H, heads, head_dim) != TRI_OK) return 0;
+  DevInfo di;
+  int sms = 148;
+  if (device_info(&di) == TRI_OK) sms = di.sms;
+  return tri::paged_attention_ws_bytes(M, H, heads, head_dim, sms);
+}
+
+tri_status tri_paged_attention(const uint16_t* q, int64_t q_stride, const int32_t* pos, const int32_t* seq,
+                               const tri_paged_cache* cache, uint16_t* out, int64_t out_stride, int64_t M, int64_t H,
+                               float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !pos || !out) return TRI_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < 1e30f)) return TRI_ERR_INVALID_ARG;
+  tri_status st = check_cache(cache);
+  if (st != TRI_OK) return st;
+  if ((st = paged_attn_shape(M, H, cache->heads, cache->head_dim)) != TRI_OK) return st;
+  const int64_t width = H * cache->head_dim;
+  if (!row_stride_ok(q_stride, width, M) || !row_stride_ok(out_stride, width, M)) return TRI_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(pos, 4) || !aligned(seq, 4)) return TRI_ERR_ALIGNMENT;
+  DevInfo di;
+  if ((st = device_info(&di)) != TRI_OK) return st;
+  const size_t need = tri::paged_attention_ws_bytes(M, H, cache->heads, cache->head_dim, di.sms);
+  if (!workspace || workspace_bytes < need) return TRI_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return TRI_ERR_ALIGNMENT;
+  return from_cuda(tri::launch_paged_attention(reinterpret_cast<const __half*>(q), q_stride, pos, seq, *cache,
+                                               reinterpret_cast<__half*>(out), out_stride, M, H, scale, workspace,
+                                               di.sms, static_cast<cudaStream_t>(stream)));
+}
+
+tri_status tri_copy_pages(void* pools, int64_t n_pools, int64_t pool_stride, int64_t pages, int64_t page_stride,
+                          int64_t page_bytes, const int32_t* src, const int32_t* dst, int64_t n, void* stream) {
+  if (!pools || n < 0 || (n > 0 && (!src || !dst))) return TRI_ERR_INVALID_ARG;
+  if (n_pools < 1 || n_pools > kMaxDim || pages < 1 || pages > kMaxDim || n > kMaxDim) return TRI_ERR_SHAPE;
+  if (page_bytes < 16 || page_bytes % 16 != 0 || page_bytes > (int64_t(1) << 32)) return TRI_ERR_SHAPE;
+  if (n > 0 && n_pools > (int64_t(1) << 40) / n) return TRI_ERR_SHAPE;
+  if (page_stride < page_bytes || page_stride % 16 != 0 || page_stride > (int64_t(1) << 40)) return TRI_ERR_SHAPE;
+  if (n_pools > 1 && (pool_stride % 16 != 0 || pool_stride < page_bytes || pool_stride > (int64_t(1) << 52)))
+    return TRI_ERR_SHAPE;
+  if (!aligned(pools, 16) || !aligned(src, 4) || !aligned(dst, 4)) return TRI_ERR_ALIGNMENT;
+  if (n == 0) return TRI_OK;
+  DevInfo di;
+  tri_status st = device_info(&di);
+  if (st != TRI_OK) return st;
+  return from_cuda(tri::launch_copy_pages(static_cast<uint8_t*>(pools), n_pools, pool_stride, pages, page_stride,
+                                          page_bytes, src, dst, n, di.sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

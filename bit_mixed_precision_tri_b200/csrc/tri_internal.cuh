@@ -76,6 +76,22 @@ cudaError_t launch_attention_decode(const __half* q, const __half* kc, const __h
                                     __half* out, int64_t M, int64_t H, int64_t Hkv, int64_t Lmax,
                                     int64_t max_len, void* ws, int sms, cudaStream_t s);
 
+// paged key/value cache (paged.cu, paged_attention.cu); `c` is checked by the caller
+cudaError_t launch_rope_table_scaled(float2* cs, int64_t Lmax, int64_t rot, double theta,
+                                     const tri_rope_scaling* sc, cudaStream_t s);
+cudaError_t launch_paged_qknorm_rope(const __half* qkv, int64_t qkv_stride, const int* pos, const int* seq,
+                                     const __half* gq, const __half* gk, const float* cs, int64_t cs_rows,
+                                     int64_t rot, bool interleaved, __half* q_out, int64_t q_stride,
+                                     const tri_paged_cache& c, int64_t T, int64_t H, float eps, int sms,
+                                     cudaStream_t s);
+cudaError_t launch_copy_pages(uint8_t* pools, int64_t n_pools, int64_t pool_stride, int64_t pages,
+                              int64_t page_stride, int64_t page_bytes, const int* src, const int* dst,
+                              int64_t n, int sms, cudaStream_t s);
+size_t paged_attention_ws_bytes(int64_t M, int64_t H, int64_t heads, int64_t head_dim, int sms);
+cudaError_t launch_paged_attention(const __half* q, int64_t q_stride, const int* pos, const int* seq,
+                                   const tri_paged_cache& c, __half* out, int64_t out_stride, int64_t M,
+                                   int64_t H, float scale, void* ws, int sms, cudaStream_t s);
+
 // decode-regime path with library-owned static scratch (no allocation)
 size_t gemv_noalloc_scratch_limit();
 size_t gemv_noalloc_scratch_need(int64_t M, int64_t N, int64_t K, int num_sms);

@@ -344,6 +344,128 @@ TRI_API tri_status tri_attention_decode(const uint16_t* q, const uint16_t* kcach
                                         int64_t Hkv, int64_t Lmax, int64_t max_len, void* workspace,
                                         size_t workspace_bytes, void* stream);
 
+/* ----------------------------------------------------------------------
+ * A paged key/value cache for the decode step.  The contiguous caches above
+ * hold Lmax positions per sequence; here positions live in pages of a shared
+ * pool that a table assigns to sequences, so that memory follows the tokens
+ * that exist, prefixes are shared and sequences fork.  The pages the library
+ * follows have no counterpart; the block's definitions (RMSNorm, QK-Norm,
+ * rotary embeddings, grouped queries) are those stated above.
+ *
+ * tri_paged_cache describes one layer's cache (host struct of device
+ * pointers, read during the call):
+ *   k, v       pools [pages][heads][page_size][head_dim], fp16 or e4m3 (1
+ *              byte, 4 exponent and 3 mantissa bits, largest 448, no
+ *              infinities); page p starts page_stride ELEMENTS after page
+ *              p - 1 (page_stride >= heads * page_size * head_dim, a multiple
+ *              of head_dim; both pools alike), 16-byte aligned.
+ *   k_scale, v_scale  e4m3 only: float32 [heads], the value of a stored
+ *              element is element * scale[head]; scales positive.
+ *   table      int32 [seqs][seq_pages], rows table_stride >= 0 elements
+ *              apart (0: one row for all): table[s][i] is the page that holds positions i * page_size ..
+ *              of sequence s.  An entry outside [0, pages) is an absent page.
+ *              One page may stand in several rows (a shared prefix).
+ *   head_dim 64 or 128; page_size a power of two, 8..256; pages <= 2^31 - 1.
+ *
+ * Rows: a call takes a batch of rows (new tokens).  Row t is position pos[t]
+ * of sequence seq[t] (device int32; seq NULL means row t is sequence t).  A
+ * row whose sequence is outside [0, seqs) or whose position is negative is
+ * padding.  Several rows may belong to one sequence (a prompt, a draft).
+ *
+ * tri_rope_table_scaled: cs[p][i] = g (cos, sin)(p * f_i), float pairs, for
+ *   p < Lmax and i < rot / 2; f_i is theta^(-2 i / rot) changed by `scaling`
+ *   (NULL: unchanged, g = 1), everything computed in float64:
+ *     TRI_ROPE_LINEAR  f_i / factor
+ *     TRI_ROPE_NTK     theta replaced by theta * factor^(rot / (rot - 2))
+ *     TRI_ROPE_BANDS   by wavelength w_i = 2 pi / f_i: w_i < context / high
+ *                      unchanged; w_i > context / low divided by factor; in
+ *                      between f_i ((1 - s) / factor + s) with
+ *                      s = (context / w_i - low) / (high - low)
+ *     TRI_ROPE_RAMP    by index: r = clamp((i - a) / (b - a), 0, 1), f_i
+ *                      ((1 - r) + r / factor), a = max(floor(c(high)), 0), b =
+ *                      min(ceil(c(low)), rot - 1), b = a + 0.001 if equal,
+ *                      c(t) = rot ln(context / (2 pi t)) / (2 ln theta);
+ *                      g = 0.1 ln(factor) + 1
+ *   rot even, 16 <= rot <= 128, rot % 16 == 0; 1 <= Lmax <= 2^24; theta > 1;
+ *   factor >= 1; BANDS and RAMP need context > 0 and 0 < low < high.
+ * tri_paged_qknorm_rope: as tri_qknorm_rope, into pages.  qkv rows
+ *   [(H + 2 heads) * head_dim] are qkv_stride elements apart.  gq, gk
+ *   [head_dim]: gains of the QK-Norm; both NULL leaves the norm out.  The
+ *   first `rot` features of every query and key head are rotated with the
+ *   table cs [cs_rows][rot / 2]: pairs (i, i + rot / 2), or (2i, 2i + 1) with
+ *   `interleaved`; the others pass.  Queries go to q_out rows (q_stride
+ *   elements apart); the key and the value go into the row's page, in e4m3
+ *   divided by the head's scale, clamped to +-448 (NaN stays NaN) and rounded
+ *   to nearest even.  A padding row, or one whose position is not below
+ *   cs_rows and seq_pages * page_size, writes nothing, q_out included; a row
+ *   whose page is absent writes its q only.  Two rows that name the same
+ *   position of the same page leave unspecified bytes there.
+ * tri_paged_attention: out[t][h] = sum_p w_p V_p / sum_p w_p, w_p =
+ *   exp(scale q[t][h] . K_p), over positions p = 0..pos[t] (at most seq_pages *
+ *   page_size of them) whose page is present; key/value head h / (H / heads),
+ *   H / heads <= 16.  A row with nothing left, padding included, gives zeros.
+ *   What the pages hold behind pos[t] does not matter (Inf and NaN included).
+ *   q and out rows q_stride and out_stride elements apart.  Nothing about the
+ *   lengths is needed on the host, so one captured graph serves every length.
+ *   workspace: tri_paged_attention_workspace_bytes (0 for shapes it refuses),
+ *   256-byte aligned, contents on entry irrelevant; calls that share one must
+ *   be ordered.  The result does not depend on the run.
+ * tri_copy_pages: for each i < n and each of n_pools pools (pool_stride bytes
+ *   apart), page dst[i] becomes a copy of page src[i]; pages are page_stride
+ *   bytes apart, page_bytes long (multiples of 16, as pool_stride).  src, dst:
+ *   device int32 [n].  A pair with an index outside [0, pages) is skipped.  A
+ *   page that stands twice in dst, or in both lists (unless src[i] = dst[i]),
+ *   ends up with unspecified bytes; other pages are not touched.  n = 0 does
+ *   nothing.
+ * Strides are multiples of 8 elements; qkv, q, q_out, out, cs and the gains are
+ * 16-byte aligned, pos, seq, table, src, dst and the scales 4-byte.  fp16
+ * results are rounded once from fp32.  Errors as above, TRI_ERR_INVALID_ARG
+ * also for a bad dtype, kind, scale or one gain without the other; nothing
+ * traps.
+ * ---------------------------------------------------------------------- */
+typedef enum tri_cache_dtype { TRI_CACHE_F16 = 0, TRI_CACHE_E4M3 = 1 } tri_cache_dtype;
+
+typedef enum tri_rope_kind {
+    TRI_ROPE_LINEAR = 1,
+    TRI_ROPE_NTK = 2,
+    TRI_ROPE_BANDS = 3,
+    TRI_ROPE_RAMP = 4
+} tri_rope_kind;
+
+typedef struct tri_rope_scaling {
+    int32_t kind;      /* one of tri_rope_kind */
+    double factor;
+    double context;    /* positions the frequencies were made for (BANDS, RAMP) */
+    double low, high;  /* BANDS: turns in `context`; RAMP: turns at the ramp's ends */
+} tri_rope_scaling;
+
+typedef struct tri_paged_cache {
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* table;
+    int64_t pages, page_size, page_stride, heads, head_dim;
+    int64_t seqs, seq_pages, table_stride;
+    int32_t dtype;     /* one of tri_cache_dtype */
+} tri_paged_cache;
+
+TRI_API tri_status tri_rope_table_scaled(float* cs, int64_t Lmax, int64_t rot, double theta,
+                                         const tri_rope_scaling* scaling, void* stream);
+TRI_API tri_status tri_paged_qknorm_rope(const uint16_t* qkv, int64_t qkv_stride, const int32_t* pos,
+                                         const int32_t* seq, const uint16_t* gq, const uint16_t* gk,
+                                         const float* cs, int64_t cs_rows, int64_t rot, int interleaved,
+                                         uint16_t* q_out, int64_t q_stride, const tri_paged_cache* cache,
+                                         int64_t T, int64_t H, float eps, void* stream);
+TRI_API size_t tri_paged_attention_workspace_bytes(int64_t M, int64_t H, int64_t heads, int64_t head_dim);
+TRI_API tri_status tri_paged_attention(const uint16_t* q, int64_t q_stride, const int32_t* pos,
+                                       const int32_t* seq, const tri_paged_cache* cache, uint16_t* out,
+                                       int64_t out_stride, int64_t M, int64_t H, float scale,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+TRI_API tri_status tri_copy_pages(void* pools, int64_t n_pools, int64_t pool_stride, int64_t pages,
+                                  int64_t page_stride, int64_t page_bytes, const int32_t* src,
+                                  const int32_t* dst, int64_t n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
