@@ -1,99 +1,730 @@
 // Attention of new tokens over a paged key/value cache:
 //   out = sum_p w_p V_p / sum_p w_p,  w_p = exp(scale q . K_p - max),
-// over the positions 0..pos of the row whose page is present.  One CTA per
-// (row, query head): 128 positions at a time, one per thread, the running
-// maximum and sum in fp32; then thread d sums feature d.
+// over the positions 0..pos of the row whose page is present.
+//
+// What bounds it: every key and value is read once for the G = H / heads query
+// heads that share it, 4 G flops per element: HBM bandwidth.
+//
+//  * Work = tiles of 64 positions of one (row, key/value head), in the order
+//    row, head, tile; every CTA takes an equal run of them, so ragged lengths
+//    load the SMs alike and the host needs no length.  A run covers the end of
+//    one (row, head), whole ones, and the start of another: whole ones are
+//    written at once, the two open ends leave a (max, sum, output) partial in
+//    the workspace, and paged_combine_kernel joins each split (row, head).
+//  * One producer warp walks the run, looks the pages up one tile ahead and
+//    loads K and V with TMA into a ring of stages (a box is one page's rows, 128
+//    bytes of each, hardware-swizzled), and the row's queries with the first
+//    tile.  Absent pages are not loaded.  A descriptor per stage says what the
+//    tile is.
+//  * Four consumer warps take 16 positions of a tile each.  Scores are formed
+//    transposed, S^T = K Q^T (mma.sync m16n8k16: positions are the 16 rows, up
+//    to 8 query heads the columns, so that no row is wasted on heads that do not
+//    exist), with the running maximum and sum in fp32 per warp.  O^T += V^T P^T:
+//    V^T comes from ldmatrix.trans, P^T from the S^T accumulators by movmatrix,
+//    in two fp16 parts (the weight and its rounding error), so that the fp32
+//    accumulation bounds the error.  e4m3 elements become fp16 (exactly) in
+//    registers; the K scale joins the softmax scale, the V scale the output.
+#include <cuda.h>
 #include <cuda_fp8.h>
+#include <cudaTypedefs.h>
 
+#include "sm100_ptx.cuh"
 #include "tri_internal.cuh"
 
 namespace tri {
 namespace {
 
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(__nv_fp8_e4m3 x) { return static_cast<float>(x); }
+using namespace ptx;
 
-template <typename E, int DH>
-__global__ void __launch_bounds__(128)
-paged_attn_simple_kernel(const __half* __restrict__ q, int64_t q_stride, const int* __restrict__ pos,
-                         const int* __restrict__ seq, const tri_paged_cache c, __half* __restrict__ out,
-                         int64_t out_stride, int H, float scale) {
-  __shared__ float qs[DH], w[128], red[4];
-  __shared__ int pg[128];
-  const int64_t m = blockIdx.x / H;
-  const int h = (int)(blockIdx.x % H), kv = h / (H / (int)c.heads), t = threadIdx.x;
-  const int ps = (int)c.page_size;
-  const int s = seq ? seq[m] : (m < c.seqs ? (int)m : -1);
-  int64_t L = (int64_t)pos[m] + 1;
-  if (s < 0 || s >= c.seqs || L < 0) L = 0;
-  if (L > c.seq_pages * ps) L = c.seq_pages * ps;
-  if (t < DH) qs[t] = __half2float(q[m * q_stride + (int64_t)h * DH + t]);
-  const float ks = c.dtype == TRI_CACHE_E4M3 ? c.k_scale[kv] : 1.f;
-  const float vs = c.dtype == TRI_CACHE_E4M3 ? c.v_scale[kv] : 1.f;
-  const E* kp = static_cast<const E*>(c.k);
-  const E* vp = static_cast<const E*>(c.v);
-  float mx = -INFINITY, l = 0.f, acc = 0.f;
-  __syncthreads();
-  for (int64_t p0 = 0; p0 < L; p0 += 128) {
-    const int64_t p = p0 + t;
-    int page = p < L ? c.table[(int64_t)s * c.table_stride + p / ps] : -1;
-    if (page >= c.pages) page = -1;
-    float sc = -INFINITY;
-    if (page >= 0) {
-      const E* row = kp + page * c.page_stride + ((int64_t)kv * ps + p % ps) * DH;
-      float d = 0.f;
-      for (int i = 0; i < DH; ++i) d = fmaf(qs[i], to_float(row[i]), d);
-      sc = d * scale * ks;
+constexpr int kTile = 64;                    // positions per stage
+constexpr int kWarps = 4;                    // consumer warps, 16 positions each
+constexpr int kThreads = 32 * (kWarps + 1);  // and the producer warp
+constexpr int kMaxStages = 8;
+constexpr uint32_t kWaitPolls = 1u << 18;    // about a second
+constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
+
+template <int DH, bool FP8, int NT>
+struct Cfg {
+  static constexpr int kRow = DH * (FP8 ? 1 : 2);             // bytes of a position
+  static constexpr int kBox = kRow < 128 ? kRow : 128;        // bytes of it in one box
+  static constexpr int kParts = kRow / kBox;
+  static constexpr int kKV = kTile * kRow;                    // bytes of a K (or V) tile
+  static constexpr int kQ = 8 * NT * DH * 2;
+  static constexpr int kMerge = 2 * DH * 8 * NT * 4;          // two warps' outputs
+  // two CTAs per SM, except 16 query heads over 256-byte rows, whose three
+  // stages, queries and merge buffer do not fit twice
+  static constexpr int kCtasPerSm = NT == 2 && kRow == 256 ? 1 : 2;
+  static constexpr int kRoom = (kCtasPerSm == 1 ? 200 : 112) * 1024 - kMerge - 2048;
+  static constexpr int kFit = kRoom / (2 * kKV + kQ);
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kSmem = 1024 + kStages * (2 * kKV + kQ) + kMerge;
+  static_assert(kStages >= 3, "a ring of three stages at least");
+};
+
+struct Desc {                 // what a stage holds
+  int row, head;              // of the batch; key/value head
+  int nval;                   // positions of the tile below the row's end
+  int pages;                  // bit i: the tile's i-th page was loaded
+  int flags;
+};
+constexpr int kFirst = 1, kLast = 2, kOpenLeft = 4, kOpenRight = 8;
+
+struct Params {
+  const __half* q;
+  const int *pos, *seq, *table;
+  const float *k_scale, *v_scale;
+  __half* out;
+  int4* recs;                 // {row * heads + head, first CTA, partials (0: not split), -}, one per
+                              // (row, head) where there are no more of them than CTAs, else per CTA
+  float2* ml;                 // [2 CTAs][8 NT] (max, sum)
+  float4* part;               // [2 CTAs][DH/16][NT][32 lanes]
+  unsigned* error;
+  int64_t q_stride, out_stride, table_stride, M;
+  int heads, G, page_shift, pages, seqs, max_len;
+  float scale;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {   // two codes in the low 16 bits
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+      ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy) : "memory");
+}
+
+// positions row m attends to, and whether it has any page table row
+__device__ __forceinline__ int row_length(const Params& p, int64_t m, int& s) {
+  s = p.seq ? p.seq[m] : (m < p.seqs ? (int)m : -1);
+  const int L = p.pos[m];
+  if (s < 0 || s >= p.seqs || L < 0) return 0;
+  return L < p.max_len ? L + 1 : p.max_len;
+}
+// a row with nothing to read still takes a tile: the one that writes its zeros
+__device__ __forceinline__ int row_tiles(int L) { return L > kTile ? (L + kTile - 1) / kTile : 1; }
+
+// the runs: the first `rem` CTAs take base + 1 tiles
+struct Runs {
+  int64_t base, rem;
+  __device__ Runs(int64_t W, int C) : base(W / C), rem(W % C) {}
+  __device__ int64_t start(int c) const { return base * c + (c < rem ? c : rem); }
+  __device__ int cta_of(int64_t w) const {
+    const int64_t big = (base + 1) * rem;
+    return (int)(w < big ? w / (base + 1) : rem + (w - big) / base);
+  }
+};
+
+template <int DH, bool FP8, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<DH, FP8, NT>::kCtasPerSm))
+paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p) {
+  using C = Cfg<DH, FP8, NT>;
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t* qring = sm + C::kStages * 2 * C::kKV;
+  float4* merge = reinterpret_cast<float4*>(qring + C::kStages * C::kQ);
+  __shared__ uint64_t full[C::kStages], empty[C::kStages];
+  __shared__ Desc desc[C::kStages];
+  __shared__ float2 wml[kWarps][8 * NT];
+  __shared__ long long sums[kWarps + 1], s_first_prefix;
+  __shared__ int s_first_row;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
     }
-    pg[t] = page;
-    float v = sc;
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    if ((t & 31) == 0) red[t >> 5] = v;
-    __syncthreads();
-    const float mnew = fmaxf(mx, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float base = mnew == -INFINITY ? 0.f : mnew;
-    const float alpha = expf(mx - base);
-    w[t] = expf(sc - base);
-    __syncthreads();
-    acc *= alpha, l *= alpha;
-    for (int i = 0; i < 128; ++i) {
-      if (pg[i] < 0) continue;
-      l += w[i];
-      if (t < DH) {
-        const E* row = vp + pg[i] * c.page_stride + ((int64_t)kv * ps + (p0 + i) % ps) * DH;
-        acc = fmaf(w[i], to_float(row[t]), acc);
+    fence_mbar_init();
+  }
+  if (warp == kWarps && lane == 0) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // ---- this CTA's run: thread t sums the tiles of M / kThreads consecutive rows
+  const int64_t chunk = (p.M + kThreads - 1) / kThreads, m_lo = tid * chunk;
+  const int64_t m_hi = m_lo + chunk < p.M ? m_lo + chunk : p.M;
+  long long mine = 0;
+  for (int64_t m = m_lo; m < m_hi; ++m) {
+    int s;
+    mine += row_tiles(row_length(p, m, s));
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w <= kWarps; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  const Runs runs(total * p.heads, gridDim.x);
+  const int64_t w0 = runs.start(blockIdx.x), ntiles = runs.start(blockIdx.x + 1) - w0;
+  if (mine > 0 && w0 >= before * p.heads && w0 < (before + mine) * p.heads) {
+    int64_t m = m_lo;
+    long long at = before;
+    for (; m < m_hi - 1; ++m) {
+      int s;
+      const int t = row_tiles(row_length(p, m, s));
+      if (w0 < (at + t) * p.heads) break;
+      at += t;
+    }
+    s_first_row = (int)m;
+    s_first_prefix = at;
+  }
+  __syncthreads();
+  if (ntiles == 0) return;
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    const uint64_t policy = policy_evict_first();
+    const int shift = p.page_shift, rows = shift < 6 ? 1 << shift : kTile;   // of a box
+    const int npg = kTile / rows, nbox = npg * C::kParts * 2;
+    const int pi = lane % npg, part = (lane / npg) % C::kParts, kv = lane / (npg * C::kParts);
+    const uint32_t box_dst = (uint32_t)(kv * C::kKV + part * kTile * C::kBox + pi * rows * C::kBox);
+    const int box_x = part * (C::kBox / (FP8 ? 1 : 2));
+    const uint32_t q_bytes = (uint32_t)(p.G * DH * 2);
+    int64_t m = s_first_row;
+    int s, L = row_length(p, m, s), T = row_tiles(L);
+    const int64_t off = w0 - (int64_t)s_first_prefix * p.heads;
+    int h = (int)(off / T), t = (int)(off % T);
+    // the next row's length, read a row ahead
+    int s_next = -1, L_next = m + 1 < p.M ? row_length(p, m + 1, s_next) : 0;
+    auto lookup = [&](int s_, int L_, int t_) -> int {     // this lane's page of a tile, -1: do not load
+      const int64_t first = (int64_t)t_ * kTile + (int64_t)pi * rows;
+      if (lane >= nbox || first >= L_) return -1;
+      const int id = p.table[(int64_t)s_ * p.table_stride + (first >> shift)];
+      return id < p.pages ? id : -1;
+    };
+    int id = lookup(s, L, t);
+    int4 split_rec = make_int4(0, 0, 0, 0);
+    uint32_t polls = kWaitPolls;
+    for (int64_t i = 0; i < ntiles; ++i) {
+      const int st = (int)(i % C::kStages);
+      const int cm = (int)m, ch = h, ct = t, cT = T, cL = L, cid = id;
+      // step on, and look the next tile's page up while this stage's slot frees
+      if (++t == T) {
+        t = 0;
+        if (++h == p.heads) {
+          h = 0, ++m, s = s_next, L = L_next, T = row_tiles(L);
+          L_next = m + 1 < p.M ? row_length(p, m + 1, s_next) : 0;
+        }
+      }
+      if (i + 1 < ntiles) id = lookup(s, L, t);
+      if (i >= C::kStages && !mbar_wait(&empty[st], (uint32_t)((i / C::kStages) - 1) & 1, polls)) {
+        if (lane == 0) record_wait_failure(p.error, kProducerCode);
+        polls = 1;
+      }
+      const bool first = i == 0 || ct == 0, last = i + 1 == ntiles || ct == cT - 1;
+      const unsigned loaded = __ballot_sync(0xFFFFFFFFu, cid >= 0);
+      if (lane == 0) {
+        Desc d;
+        d.row = cm, d.head = ch;
+        const int64_t left = (int64_t)cL - (int64_t)ct * kTile;
+        d.nval = left < 0 ? 0 : (left < kTile ? (int)left : kTile);
+        d.pages = (int)(loaded & ((1u << npg) - 1));       // lanes 0.. hold K's first part of page 0..
+        d.flags = (first ? kFirst : 0) | (last ? kLast : 0);
+        if (last) {
+          const bool open_l = i - ct < 0;                  // the (row, head) began before this run
+          const bool open_r = ct != cT - 1;
+          d.flags |= (open_l ? kOpenLeft : 0) | (open_r ? kOpenRight : 0);
+        }
+        desc[st] = d;
+        // the CTA that holds the first tile of a (row, head) says who joins it
+        if (ct == 0) {
+          const int64_t seg = (int64_t)cm * p.heads + ch, segs = p.M * p.heads, end = i + cT;
+          const bool split = end > ntiles;
+          const int4 rec = make_int4((int)seg, (int)blockIdx.x,
+                                     split ? runs.cta_of(w0 + end - 1) - (int)blockIdx.x + 1 : 0, 0);
+          if (segs <= gridDim.x) p.recs[seg] = rec;
+          else if (split) split_rec = rec;
+        }
+        mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(loaded) * rows * C::kBox + (first ? q_bytes : 0u));
+        if (first)
+          bulk_load(qring + st * C::kQ, p.q + (int64_t)cm * p.q_stride + (int64_t)ch * p.G * DH, q_bytes, &full[st]);
+      }
+      __syncwarp();
+      if (cid >= 0) {
+        const int in_page = shift > 6 ? (int)(((int64_t)ct * kTile) & ((1 << shift) - 1)) : 0;
+        tma_load_3d(smem_u32(sm) + (uint32_t)(st * 2 * C::kKV) + box_dst, kv ? &vmap : &kmap, box_x,
+                    (ch << shift) + in_page, cid, &full[st], policy);
       }
     }
-    mx = mnew;
-    __syncthreads();
+    if (lane == 0 && p.M * p.heads > gridDim.x) p.recs[blockIdx.x] = split_rec;
+    // every copy has landed before the CTA may leave
+    for (int64_t i = ntiles > C::kStages ? ntiles - C::kStages : 0; i < ntiles; ++i)
+      if (!mbar_wait(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1, kWaitPolls) && lane == 0)
+        record_wait_failure(p.error, kDrainCode);
+    return;
   }
-  if (t < DH) out[m * out_stride + (int64_t)h * DH + t] = __float2half_rn(l == 0.f ? 0.f : acc / l * vs);
+
+  // -------------------------------------------------------------- consumers
+  const int gid = lane >> 2, tig = lane & 3;
+  const int page_shift = p.page_shift < 6 ? p.page_shift : 6;
+  // ldmatrix rows and 16-byte chunks: K (and e4m3 V): rows (lane & 7) + 8 (lane
+  // >> 3 & 1), chunk + (lane >> 4); fp16 V transposed: rows (lane & 7) + 8 (lane
+  // >> 4), chunk + (lane >> 3 & 1)
+  const int r_a = 16 * warp + (lane & 7) + 8 * ((lane >> 3) & 1), c_a = lane >> 4;
+  const int r_t = 16 * warp + (lane & 7) + 8 * (lane >> 4), c_t = (lane >> 3) & 1;
+  auto address = [&](uint32_t base, int row, int chunk) -> uint32_t {
+    if constexpr (C::kBox == 128)
+      return base + (uint32_t)((chunk >> 3) * kTile * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+    else
+      return base + (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+  };
+  uint32_t qf[DH / 16][NT][2];
+  float o[DH / 16][NT][4];
+  float mx[NT][2], l[NT][2];
+  float c2 = 0.f;
+  uint32_t polls = kWaitPolls;
+  for (int64_t i = 0; i < ntiles; ++i) {
+    const int st = (int)(i % C::kStages);
+    if (!mbar_wait(&full[st], (uint32_t)(i / C::kStages) & 1, polls)) {
+      if (lane == 0) record_wait_failure(p.error, kConsumerCode);
+      polls = 1;
+    }
+    __syncwarp();
+    const Desc d = desc[st];
+    const uint32_t kbase = smem_u32(sm) + (uint32_t)(st * 2 * C::kKV), vbase = kbase + C::kKV;
+    if (d.flags & kFirst) {
+      const uint32_t qb = smem_u32(qring + st * C::kQ);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hd = 8 * nt + gid;
+        const bool real = hd < p.G;
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          // fp16: features 2 tig, +1 and 8 + 2 tig, +1 of the step; e4m3: 4 tig .. 4 tig + 3,
+          // the order in which a lane gets its four bytes of K
+          const uint32_t a = qb + (uint32_t)(hd * DH * 2 + kk * 32 + (FP8 ? 8 : 4) * tig);
+          qf[kk][nt][0] = real ? lds32(a) : 0u;
+          qf[kk][nt][1] = real ? lds32(a + (FP8 ? 4 : 16)) : 0u;
+        }
+        mx[nt][0] = mx[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int fb = 0; fb < DH / 16; ++fb) o[fb][nt][0] = o[fb][nt][1] = o[fb][nt][2] = o[fb][nt][3] = 0.f;
+      }
+      c2 = p.scale * 1.4426950408889634f * (FP8 ? p.k_scale[d.head] : 1.f);
+    }
+    // ---- S^T = K Q^T
+    float sc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+    if constexpr (FP8) {
+#pragma unroll
+      for (int kp = 0; kp < DH / 32; ++kp) {
+        uint32_t r[4];
+        ldsm_x4(address(kbase, r_a, 2 * kp + c_a), r);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t a[4] = {e4m3x2_to_half2(r[2 * k] & 0xFFFFu), e4m3x2_to_half2(r[2 * k + 1] & 0xFFFFu),
+                                 e4m3x2_to_half2(r[2 * k] >> 16), e4m3x2_to_half2(r[2 * k + 1] >> 16)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816(sc[nt], a, qf[2 * kp + k][nt][0], qf[2 * kp + k][nt][1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        uint32_t a[4];
+        ldsm_x4(address(kbase, r_a, 2 * kk + c_a), a);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16816(sc[nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+      }
+    }
+    // ---- the tile's valid positions: this lane's two, and those of its V rows
+    const bool whole = d.nval == kTile && d.pages == (1 << (kTile >> page_shift)) - 1;
+    auto valid = [&](int r) { return r < d.nval && ((d.pages >> (r >> page_shift)) & 1); };
+    if (!whole) {
+      const bool v0 = valid(16 * warp + gid), v1 = valid(16 * warp + gid + 8);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (!v0) sc[nt][0] = sc[nt][1] = -INFINITY;
+        if (!v1) sc[nt][2] = sc[nt][3] = -INFINITY;
+      }
+    }
+    // ---- running softmax; the eight lanes of a column hold its 16 positions
+    uint32_t ph[NT][2], pl[NT][2];
+    bool grew = false;
+    float alpha[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = fmaxf(sc[nt][e], sc[nt][2 + e]) * c2;
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+        const float mnew = fmaxf(mx[nt][e], top);
+        const float base = mnew == -INFINITY ? 0.f : mnew;       // nothing seen yet: all weights 0
+        alpha[nt][e] = ex2(mx[nt][e] - base);
+        grew |= mnew > mx[nt][e];
+        mx[nt][e] = mnew;
+        pr[e] = ex2(fmaf(sc[nt][e], c2, -base));
+        pr[2 + e] = ex2(fmaf(sc[nt][2 + e], c2, -base));
+      }
+      ph[nt][0] = half2_bits(pr[0], pr[1]);
+      ph[nt][1] = half2_bits(pr[2], pr[3]);
+      const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&ph[nt][0]));
+      const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&ph[nt][1]));
+      pl[nt][0] = transpose8x8(half2_bits(pr[0] - h0.x, pr[1] - h0.y));
+      pl[nt][1] = transpose8x8(half2_bits(pr[2] - h1.x, pr[3] - h1.y));
+      ph[nt][0] = transpose8x8(ph[nt][0]);
+      ph[nt][1] = transpose8x8(ph[nt][1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) l[nt][e] = fmaf(l[nt][e], alpha[nt][e], pr[e] + pr[2 + e]);
+    }
+    if (__any_sync(0xFFFFFFFFu, grew)) {                         // rare after the first tiles
+#pragma unroll
+      for (int fb = 0; fb < DH / 16; ++fb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[fb][nt][0] *= alpha[nt][0], o[fb][nt][1] *= alpha[nt][1];
+          o[fb][nt][2] *= alpha[nt][0], o[fb][nt][3] *= alpha[nt][1];
+        }
+    }
+    // ---- O^T += V^T P^T.  A weight of zero times the NaN of a position that does
+    // not count would be NaN, so such V rows are cleared (the 16-bit halves of a
+    // register are two neighbouring positions)
+    uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
+    if (!whole) {
+      const int r = 16 * warp + 2 * tig;
+      m0 = (valid(r) ? 0xFFFFu : 0u) | (valid(r + 1) ? 0xFFFF0000u : 0u);
+      m1 = (valid(r + 8) ? 0xFFFFu : 0u) | (valid(r + 9) ? 0xFFFF0000u : 0u);
+    }
+    if constexpr (FP8) {
+#pragma unroll
+      for (int fp = 0; fp < DH / 32; ++fp) {
+        uint32_t r[4];
+        ldsm_x4_t(address(vbase, r_a, 2 * fp + c_a), r);
+        r[0] &= m0, r[1] &= m1, r[2] &= m0, r[3] &= m1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          // bytes: (position 2 tig: features 2 gid, 2 gid + 1), (position 2 tig + 1: the same)
+          const uint32_t a[4] = {e4m3x2_to_half2(__byte_perm(r[2 * k], 0, 0x4420)),
+                                 e4m3x2_to_half2(__byte_perm(r[2 * k], 0, 0x4431)),
+                                 e4m3x2_to_half2(__byte_perm(r[2 * k + 1], 0, 0x4420)),
+                                 e4m3x2_to_half2(__byte_perm(r[2 * k + 1], 0, 0x4431))};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(o[2 * fp + k][nt], a, ph[nt][0], ph[nt][1]);
+            mma_16816(o[2 * fp + k][nt], a, pl[nt][0], pl[nt][1]);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int fb = 0; fb < DH / 16; ++fb) {
+        uint32_t a[4];
+        ldsm_x4_t(address(vbase, r_t, 2 * fb + c_t), a);
+        a[0] &= m0, a[1] &= m0, a[2] &= m1, a[3] &= m1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816(o[fb][nt], a, ph[nt][0], ph[nt][1]);
+          mma_16816(o[fb][nt], a, pl[nt][0], pl[nt][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+    if (!(d.flags & kLast)) continue;
+
+    // ---- the four warps' (max, sum, output) into one, in warp order
+    float f[NT][2], lsum[NT][2], mtop[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = l[nt][e];
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        if (gid == 0) wml[warp][8 * nt + 2 * tig + e] = make_float2(mx[nt][e], v);
+      }
+    named_bar_sync(1, 32 * kWarps);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hd = 8 * nt + 2 * tig + e;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, wml[w][hd].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum = fmaf(wml[w][hd].y, ex2(wml[w][hd].x - base), sum);
+        f[nt][e] = ex2(mx[nt][e] - base);
+        lsum[nt][e] = sum;
+        mtop[nt][e] = top;
+      }
+#pragma unroll
+    for (int fb = 0; fb < DH / 16; ++fb)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        o[fb][nt][0] *= f[nt][0], o[fb][nt][1] *= f[nt][1];
+        o[fb][nt][2] *= f[nt][0], o[fb][nt][3] *= f[nt][1];
+      }
+    constexpr int kVec = DH / 16 * NT * 32;                      // float4s of one warp's output
+    auto put = [&](float4* dst) {
+#pragma unroll
+      for (int fb = 0; fb < DH / 16; ++fb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          dst[(fb * NT + nt) * 32 + lane] = make_float4(o[fb][nt][0], o[fb][nt][1], o[fb][nt][2], o[fb][nt][3]);
+    };
+    auto add = [&](const float4* src) {
+#pragma unroll
+      for (int fb = 0; fb < DH / 16; ++fb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float4 v = src[(fb * NT + nt) * 32 + lane];
+          o[fb][nt][0] += v.x, o[fb][nt][1] += v.y, o[fb][nt][2] += v.z, o[fb][nt][3] += v.w;
+        }
+    };
+    if (warp >= 2) put(merge + (warp - 2) * kVec);
+    named_bar_sync(1, 32 * kWarps);
+    if (warp < 2) add(merge + warp * kVec);
+    if (warp == 1) put(merge + kVec);
+    named_bar_sync(1, 32 * kWarps);
+    if (warp != 0) continue;
+    add(merge + kVec);
+    if (d.flags & (kOpenLeft | kOpenRight)) {
+      const int64_t slot = 2 * (int64_t)blockIdx.x + ((d.flags & kOpenLeft) ? 0 : 1);
+      put(p.part + slot * kVec);
+      if (gid == 0)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            p.ml[slot * 8 * NT + 8 * nt + 2 * tig + e] = make_float2(mtop[nt][e], lsum[nt][e]);
+    } else {
+      const float vs = FP8 ? p.v_scale[d.head] : 1.f;
+      __half* dst = p.out + (int64_t)d.row * p.out_stride + (int64_t)d.head * p.G * DH;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int hd = 8 * nt + 2 * tig + e;
+          if (hd >= p.G) continue;
+          const float inv = lsum[nt][e] == 0.f ? 0.f : vs / lsum[nt][e];
+#pragma unroll
+          for (int fb = 0; fb < DH / 16; ++fb) {
+            if constexpr (FP8) {
+              *reinterpret_cast<__half2*>(dst + hd * DH + 16 * fb + 2 * gid) =
+                  __floats2half2_rn(o[fb][nt][e] * inv, o[fb][nt][2 + e] * inv);
+            } else {
+              dst[hd * DH + 16 * fb + gid] = __float2half_rn(o[fb][nt][e] * inv);
+              dst[hd * DH + 16 * fb + 8 + gid] = __float2half_rn(o[fb][nt][2 + e] * inv);
+            }
+          }
+        }
+    }
+  }
+}
+
+// Joins the partials of each split (row, head), in CTA order.  CTA (x, y): the
+// x-th record, float4s 32 y .. 32 y + 31 of the output; warp w sums every 8th
+// partial, then the eight sums are added in warp order.
+constexpr int kCombineThreads = 256;
+
+template <int DH, bool FP8, int NT>
+__global__ void __launch_bounds__(kCombineThreads)
+paged_combine_kernel(const Params p) {
+  extern __shared__ float wts[];                                 // [partials][8 NT]
+  __shared__ float inv[8 * NT];
+  __shared__ float4 sums[8][32];
+  constexpr int kVec = DH / 16 * NT * 32;
+  griddep_wait();                                                // in every CTA: the grid ends after its predecessor
+  const int4 rec = p.recs[blockIdx.x];
+  const int J = rec.z;
+  if (J == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = rec.x / p.heads, head = rec.x % p.heads;
+  auto slot = [&](int j) -> int64_t { return 2 * (int64_t)(rec.y + j) + (j == 0 ? 1 : 0); };
+  for (int hd = warp; hd < 8 * NT; hd += 8) {
+    float top = -INFINITY;
+    for (int j = lane; j < J; j += 32) top = fmaxf(top, p.ml[slot(j) * 8 * NT + hd].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    for (int j = lane; j < J; j += 32) {
+      const float2 v = p.ml[slot(j) * 8 * NT + hd];
+      const float w = ex2(v.x - base);
+      wts[j * 8 * NT + hd] = w;
+      sum = fmaf(w, v.y, sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) inv[hd] = sum == 0.f ? 0.f : (FP8 ? p.v_scale[head] : 1.f) / sum;
+  }
+  __syncthreads();
+  const int vec = blockIdx.y * 32 + lane, block = vec >> 5, fb = block / NT, nt = block % NT;
+  const int gid = lane >> 2, tig = lane & 3, h0 = 8 * nt + 2 * tig;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = warp; j < J; j += 8) {
+    const float4 v = p.part[slot(j) * kVec + vec];
+    const float a = wts[j * 8 * NT + h0], b = wts[j * 8 * NT + h0 + 1];
+    acc.x = fmaf(a, v.x, acc.x), acc.y = fmaf(b, v.y, acc.y);
+    acc.z = fmaf(a, v.z, acc.z), acc.w = fmaf(b, v.w, acc.w);
+  }
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) {
+    const float4 v = sums[w][lane];
+    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+  }
+  __half* dst = p.out + (int64_t)row * p.out_stride + (int64_t)head * p.G * DH;
+  const int f0 = 16 * fb + (FP8 ? 2 * gid : gid), f1 = 16 * fb + (FP8 ? 2 * gid + 1 : 8 + gid);
+  if (h0 < p.G) {
+    dst[h0 * DH + f0] = __float2half_rn(acc.x * inv[h0]);
+    dst[h0 * DH + f1] = __float2half_rn(acc.z * inv[h0]);
+  }
+  if (h0 + 1 < p.G) {
+    dst[(h0 + 1) * DH + f0] = __float2half_rn(acc.y * inv[h0 + 1]);
+    dst[(h0 + 1) * DH + f1] = __float2half_rn(acc.w * inv[h0 + 1]);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn_p() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    return nullptr;
+  }();
+  return fn;
+}
+
+constexpr int kMaxCtasPerSm = 2;
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Space {
+  size_t ml, part, total;
+};
+Space space(int64_t ctas, int64_t nt, int64_t dh) {
+  Space w;
+  w.ml = up256((size_t)ctas * sizeof(int4));
+  w.part = w.ml + up256((size_t)(2 * ctas * 8 * nt) * sizeof(float2));
+  w.total = w.part + (size_t)(2 * ctas * 8 * nt * dh) * sizeof(float);
+  return w;
+}
+
+template <int DH, bool FP8, int NT>
+cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaStream_t s) {
+  using K = Cfg<DH, FP8, NT>;
+  auto enc = encode_fn_p();
+  if (!enc) return cudaErrorNotSupported;
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t dims[3] = {(cuuint64_t)DH, (cuuint64_t)(c.heads * c.page_size), (cuuint64_t)c.pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)K::kRow, (cuuint64_t)c.page_stride * (FP8 ? 1 : 2)};
+    const cuuint32_t box[3] = {(cuuint32_t)(K::kBox / (FP8 ? 1 : 2)),
+                               (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile), 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    if (enc(&maps[i], FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, i ? c.v : c.k, dims,
+            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            K::kBox == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = wait_status_word(&p.error);
+  if (e != cudaSuccess) return e;
+  static bool ready[64] = {};
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(paged_attn_kernel<DH, FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  // no more CTAs than tiles can exist
+  const int64_t most = p.M * p.heads * (int64_t)((p.max_len + kTile - 1) / kTile);
+  const int64_t ctas = most < (int64_t)K::kCtasPerSm * sms ? most : (int64_t)K::kCtasPerSm * sms;
+  const Space w = space(ctas, NT, DH);
+  p.recs = static_cast<int4*>(ws);
+  p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + w.ml);
+  p.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + w.part);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = K::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<DH, FP8, NT>, maps[0], maps[1], p)) != cudaSuccess) return e;
+  const int64_t segs = p.M * p.heads;
+  cfg.gridDim = dim3((unsigned)(segs < ctas ? segs : ctas), DH / 16 * NT);
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.dynamicSmemBytes = (size_t)ctas * 8 * NT * sizeof(float);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<DH, FP8, NT>, p);
 }
 
 }  // namespace
 
-size_t paged_attention_ws_bytes(int64_t, int64_t, int64_t, int64_t, int) { return 256; }
+size_t paged_attention_ws_bytes(int64_t, int64_t H, int64_t heads, int64_t head_dim, int sms) {
+  return up256(space((int64_t)kMaxCtasPerSm * sms, H / heads > 8 ? 2 : 1, head_dim).total);
+}
 
 cudaError_t launch_paged_attention(const __half* q, int64_t q_stride, const int* pos, const int* seq,
                                    const tri_paged_cache& c, __half* out, int64_t out_stride, int64_t M,
-                                   int64_t H, float scale, void*, int, cudaStream_t s) {
-  const unsigned grid = (unsigned)(M * H);
-  if (c.dtype == TRI_CACHE_E4M3) {
-    if (c.head_dim == 128)
-      paged_attn_simple_kernel<__nv_fp8_e4m3, 128><<<grid, 128, 0, s>>>(q, q_stride, pos, seq, c, out, out_stride,
-                                                                         (int)H, scale);
-    else
-      paged_attn_simple_kernel<__nv_fp8_e4m3, 64><<<grid, 128, 0, s>>>(q, q_stride, pos, seq, c, out, out_stride,
-                                                                        (int)H, scale);
-  } else {
-    if (c.head_dim == 128)
-      paged_attn_simple_kernel<__half, 128><<<grid, 128, 0, s>>>(q, q_stride, pos, seq, c, out, out_stride, (int)H,
-                                                                 scale);
-    else
-      paged_attn_simple_kernel<__half, 64><<<grid, 128, 0, s>>>(q, q_stride, pos, seq, c, out, out_stride, (int)H,
-                                                                scale);
+                                   int64_t H, float scale, void* ws, int sms, cudaStream_t s) {
+  Params p = {};
+  p.q = q, p.pos = pos, p.seq = seq, p.table = c.table, p.k_scale = c.k_scale, p.v_scale = c.v_scale, p.out = out;
+  p.q_stride = q_stride, p.out_stride = out_stride, p.table_stride = c.table_stride, p.M = M;
+  p.heads = (int)c.heads, p.G = (int)(H / c.heads), p.pages = (int)c.pages, p.seqs = (int)c.seqs;
+  p.max_len = (int)(c.seq_pages * c.page_size), p.scale = scale;
+  while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
+  const bool fp8 = c.dtype == TRI_CACHE_E4M3, wide = p.G > 8;
+  if (c.head_dim == 128) {
+    if (fp8) return wide ? launch<128, true, 2>(p, c, ws, sms, s) : launch<128, true, 1>(p, c, ws, sms, s);
+    return wide ? launch<128, false, 2>(p, c, ws, sms, s) : launch<128, false, 1>(p, c, ws, sms, s);
   }
-  return cudaGetLastError();
+  if (fp8) return wide ? launch<64, true, 2>(p, c, ws, sms, s) : launch<64, true, 1>(p, c, ws, sms, s);
+  return wide ? launch<64, false, 2>(p, c, ws, sms, s) : launch<64, false, 1>(p, c, ws, sms, s);
 }
 
 }  // namespace tri
