@@ -49,12 +49,13 @@ struct Cfg {
   static constexpr int kBox = kRow < 128 ? kRow : 128;        // bytes of it in one box
   static constexpr int kParts = kRow / kBox;
   static constexpr int kKV = kTile * kRow;                    // bytes of a K (or V) tile
-  static constexpr int kQ = 8 * NT * DH * 2;
+  static constexpr int kQRow = DH * 2 + 16;                   // padded: fragment reads hit distinct banks
+  static constexpr int kQ = 8 * NT * kQRow;
   static constexpr int kMerge = 2 * DH * 8 * NT * 4;          // two warps' outputs
   // two CTAs per SM, except 16 query heads over 256-byte rows, whose three
   // stages, queries and merge buffer do not fit twice
   static constexpr int kCtasPerSm = NT == 2 && kRow == 256 ? 1 : 2;
-  static constexpr int kRoom = (kCtasPerSm == 1 ? 200 : 112) * 1024 - kMerge - 2048;
+  static constexpr int kRoom = (kCtasPerSm == 1 ? 200 : 113) * 1024 - kMerge - 2560;
   static constexpr int kFit = kRoom / (2 * kKV + kQ);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kSmem = 1024 + kStages * (2 * kKV + kQ) + kMerge;
@@ -106,9 +107,10 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {   // two codes in the low 16 bits
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// four e4m3 codes as fp16: bytes 0, 1 and bytes 2, 3
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(four));
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar,
                                             uint64_t policy) {
@@ -125,8 +127,7 @@ __device__ __forceinline__ int row_length(const Params& p, int64_t m, int& s) {
   if (s < 0 || s >= p.seqs || L < 0) return 0;
   return L < p.max_len ? L + 1 : p.max_len;
 }
-// a row with nothing to read still takes a tile: the one that writes its zeros
-__device__ __forceinline__ int row_tiles(int L) { return L > kTile ? (L + kTile - 1) / kTile : 1; }
+__device__ __forceinline__ int row_tiles(int L) { return (L + kTile - 1) / kTile; }
 
 // the runs: the first `rem` CTAs take base + 1 tiles
 struct Runs {
@@ -138,6 +139,20 @@ struct Runs {
     return (int)(w < big ? w / (base + 1) : rem + (w - big) / base);
   }
 };
+
+// a lane's four sums of a feature block: heads h0 and h0 + 1 of (x, z) and (y, w)
+template <int DH, bool FP8>
+__device__ __forceinline__ void store_out(__half* dst, int h0, int G, int f, int gid, float4 y, float i0, float i1) {
+  const int f0 = f + (FP8 ? 2 * gid : gid), f1 = f + (FP8 ? 2 * gid + 1 : 8 + gid);
+  if (h0 < G) {
+    dst[h0 * DH + f0] = __float2half_rn(y.x * i0);
+    dst[h0 * DH + f1] = __float2half_rn(y.z * i0);
+  }
+  if (h0 + 1 < G) {
+    dst[(h0 + 1) * DH + f0] = __float2half_rn(y.y * i1);
+    dst[(h0 + 1) * DH + f1] = __float2half_rn(y.w * i1);
+  }
+}
 
 template <int DH, bool FP8, int NT>
 __global__ void __launch_bounds__(kThreads, (Cfg<DH, FP8, NT>::kCtasPerSm))
@@ -205,7 +220,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     s_first_prefix = at;
   }
   __syncthreads();
-  if (ntiles == 0) return;
+  // rows with nothing to read take no tiles: their zeros are dealt out by row
+  const bool by_seg = p.M * p.heads <= gridDim.x;               // see Params::recs
+  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+    int s;
+    if (row_length(p, m, s) > 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(p.out + m * p.out_stride);
+    for (int i = tid; i < p.heads * p.G * (DH / 8); i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
+    if (by_seg)
+      for (int i = tid; i < p.heads; i += kThreads) p.recs[m * p.heads + i] = make_int4(0, 0, 0, 0);
+  }
+  if (ntiles == 0) {
+    if (!by_seg && tid == 0) p.recs[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
@@ -215,7 +243,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int pi = lane % npg, part = (lane / npg) % C::kParts, kv = lane / (npg * C::kParts);
     const uint32_t box_dst = (uint32_t)(kv * C::kKV + part * kTile * C::kBox + pi * rows * C::kBox);
     const int box_x = part * (C::kBox / (FP8 ? 1 : 2));
-    const uint32_t q_bytes = (uint32_t)(p.G * DH * 2);
     int64_t m = s_first_row;
     int s, L = row_length(p, m, s), T = row_tiles(L);
     const int64_t off = w0 - (int64_t)s_first_prefix * p.heads;
@@ -231,19 +258,25 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     int id = lookup(s, L, t);
     int4 split_rec = make_int4(0, 0, 0, 0);
     uint32_t polls = kWaitPolls;
-    for (int64_t i = 0; i < ntiles; ++i) {
-      const int st = (int)(i % C::kStages);
+    int st = 0;
+    uint32_t phase = 1;                                         // of `empty`; nothing to wait for in the first round
+    for (int64_t i = 0; i < ntiles; ++i, ++st) {
+      if (st == C::kStages) st = 0, phase ^= 1;
       const int cm = (int)m, ch = h, ct = t, cT = T, cL = L, cid = id;
       // step on, and look the next tile's page up while this stage's slot frees
       if (++t == T) {
         t = 0;
         if (++h == p.heads) {
-          h = 0, ++m, s = s_next, L = L_next, T = row_tiles(L);
-          L_next = m + 1 < p.M ? row_length(p, m + 1, s_next) : 0;
+          h = 0;
+          do {                                                  // the next row that has anything
+            ++m, s = s_next, L = L_next;
+            L_next = m + 1 < p.M ? row_length(p, m + 1, s_next) : 0;
+          } while (L == 0 && m + 1 < p.M);
+          T = row_tiles(L);
         }
       }
       if (i + 1 < ntiles) id = lookup(s, L, t);
-      if (i >= C::kStages && !mbar_wait(&empty[st], (uint32_t)((i / C::kStages) - 1) & 1, polls)) {
+      if (i >= C::kStages && !mbar_wait(&empty[st], phase, polls)) {
         if (lane == 0) record_wait_failure(p.error, kProducerCode);
         polls = 1;
       }
@@ -264,25 +297,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         desc[st] = d;
         // the CTA that holds the first tile of a (row, head) says who joins it
         if (ct == 0) {
-          const int64_t seg = (int64_t)cm * p.heads + ch, segs = p.M * p.heads, end = i + cT;
+          const int64_t seg = (int64_t)cm * p.heads + ch, end = i + cT;
           const bool split = end > ntiles;
           const int4 rec = make_int4((int)seg, (int)blockIdx.x,
                                      split ? runs.cta_of(w0 + end - 1) - (int)blockIdx.x + 1 : 0, 0);
-          if (segs <= gridDim.x) p.recs[seg] = rec;
+          if (by_seg) p.recs[seg] = rec;
           else if (split) split_rec = rec;
         }
-        mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(loaded) * rows * C::kBox + (first ? q_bytes : 0u));
-        if (first)
-          bulk_load(qring + st * C::kQ, p.q + (int64_t)cm * p.q_stride + (int64_t)ch * p.G * DH, q_bytes, &full[st]);
+        mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(loaded) * rows * C::kBox + (first ? p.G * DH * 2 : 0)));
       }
       __syncwarp();
+      if (first && lane < p.G)
+        bulk_load(qring + st * C::kQ + lane * C::kQRow, p.q + (int64_t)cm * p.q_stride + ((int64_t)ch * p.G + lane) * DH,
+                  DH * 2, &full[st]);
       if (cid >= 0) {
         const int in_page = shift > 6 ? (int)(((int64_t)ct * kTile) & ((1 << shift) - 1)) : 0;
         tma_load_3d(smem_u32(sm) + (uint32_t)(st * 2 * C::kKV) + box_dst, kv ? &vmap : &kmap, box_x,
                     (ch << shift) + in_page, cid, &full[st], policy);
       }
     }
-    if (lane == 0 && p.M * p.heads > gridDim.x) p.recs[blockIdx.x] = split_rec;
+    if (lane == 0 && !by_seg) p.recs[blockIdx.x] = split_rec;
     // every copy has landed before the CTA may leave
     for (int64_t i = ntiles > C::kStages ? ntiles - C::kStages : 0; i < ntiles; ++i)
       if (!mbar_wait(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1, kWaitPolls) && lane == 0)
@@ -308,10 +342,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   float o[DH / 16][NT][4];
   float mx[NT][2], l[NT][2];
   float c2 = 0.f;
-  uint32_t polls = kWaitPolls;
-  for (int64_t i = 0; i < ntiles; ++i) {
-    const int st = (int)(i % C::kStages);
-    if (!mbar_wait(&full[st], (uint32_t)(i / C::kStages) & 1, polls)) {
+  uint32_t polls = kWaitPolls, phase = 0;
+  int st = 0;
+  for (int64_t i = 0; i < ntiles; ++i, ++st) {
+    if (st == C::kStages) st = 0, phase ^= 1;
+    if (!mbar_wait(&full[st], phase, polls)) {
       if (lane == 0) record_wait_failure(p.error, kConsumerCode);
       polls = 1;
     }
@@ -328,7 +363,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (int kk = 0; kk < DH / 16; ++kk) {
           // fp16: features 2 tig, +1 and 8 + 2 tig, +1 of the step; e4m3: 4 tig .. 4 tig + 3,
           // the order in which a lane gets its four bytes of K
-          const uint32_t a = qb + (uint32_t)(hd * DH * 2 + kk * 32 + (FP8 ? 8 : 4) * tig);
+          const uint32_t a = qb + (uint32_t)(hd * C::kQRow + kk * 32 + (FP8 ? 8 : 4) * tig);
           qf[kk][nt][0] = real ? lds32(a) : 0u;
           qf[kk][nt][1] = real ? lds32(a + (FP8 ? 4 : 16)) : 0u;
         }
@@ -340,9 +375,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       c2 = p.scale * 1.4426950408889634f * (FP8 ? p.k_scale[d.head] : 1.f);
     }
     // ---- S^T = K Q^T
-    float sc[NT][4];
+    float sc[NT][4], sc1[NT][4];                                 // two chains of dependent MMAs
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[nt][e] = sc1[nt][e] = 0.f;
     if constexpr (FP8) {
 #pragma unroll
       for (int kp = 0; kp < DH / 32; ++kp) {
@@ -350,10 +387,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         ldsm_x4(address(kbase, r_a, 2 * kp + c_a), r);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t a[4] = {e4m3x2_to_half2(r[2 * k] & 0xFFFFu), e4m3x2_to_half2(r[2 * k + 1] & 0xFFFFu),
-                                 e4m3x2_to_half2(r[2 * k] >> 16), e4m3x2_to_half2(r[2 * k + 1] >> 16)};
+          uint32_t a[4];
+          e4m3x4_to_half2(r[2 * k], a[0], a[2]);
+          e4m3x4_to_half2(r[2 * k + 1], a[1], a[3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(sc[nt], a, qf[2 * kp + k][nt][0], qf[2 * kp + k][nt][1]);
+          for (int nt = 0; nt < NT; ++nt) mma_16816(k ? sc1[nt] : sc[nt], a, qf[2 * kp + k][nt][0], qf[2 * kp + k][nt][1]);
         }
       }
     } else {
@@ -362,19 +400,33 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         uint32_t a[4];
         ldsm_x4(address(kbase, r_a, 2 * kk + c_a), a);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816(sc[nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_16816(kk & 1 ? sc1[nt] : sc[nt], a, qf[kk][nt][0], qf[kk][nt][1]);
       }
     }
-    // ---- the tile's valid positions: this lane's two, and those of its V rows
-    const bool whole = d.nval == kTile && d.pages == (1 << (kTile >> page_shift)) - 1;
-    auto valid = [&](int r) { return r < d.nval && ((d.pages >> (r >> page_shift)) & 1); };
-    if (!whole) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[nt][e] += sc1[nt][e];
+    // ---- positions that do not count (behind the row's end, in absent pages): no
+    // weight, and a weight of zero times a NaN would be NaN, so their V rows are
+    // cleared in the stage before they are read
+    if (d.nval != kTile || d.pages != (1 << (kTile >> page_shift)) - 1) {
+      auto valid = [&](int r) { return r < d.nval && ((d.pages >> (r >> page_shift)) & 1); };
       const bool v0 = valid(16 * warp + gid), v1 = valid(16 * warp + gid + 8);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (!v0) sc[nt][0] = sc[nt][1] = -INFINITY;
         if (!v1) sc[nt][2] = sc[nt][3] = -INFINITY;
       }
+      const int r = 16 * warp + (lane >> 1);                     // two lanes a row
+      if (!valid(r))
+#pragma unroll
+        for (int c = 0; c < C::kRow / 32; ++c) {
+          const uint32_t a = address(vbase, r, 2 * c + (lane & 1));
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+        }
+      fence_proxy_async();                                       // before TMA refills the stage
+      __syncwarp();
     }
     // ---- running softmax; the eight lanes of a column hold its 16 positions
     uint32_t ph[NT][2], pl[NT][2];
@@ -417,28 +469,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           o[fb][nt][2] *= alpha[nt][0], o[fb][nt][3] *= alpha[nt][1];
         }
     }
-    // ---- O^T += V^T P^T.  A weight of zero times the NaN of a position that does
-    // not count would be NaN, so such V rows are cleared (the 16-bit halves of a
-    // register are two neighbouring positions)
-    uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
-    if (!whole) {
-      const int r = 16 * warp + 2 * tig;
-      m0 = (valid(r) ? 0xFFFFu : 0u) | (valid(r + 1) ? 0xFFFF0000u : 0u);
-      m1 = (valid(r + 8) ? 0xFFFFu : 0u) | (valid(r + 9) ? 0xFFFF0000u : 0u);
-    }
+    // ---- O^T += V^T P^T
     if constexpr (FP8) {
 #pragma unroll
       for (int fp = 0; fp < DH / 32; ++fp) {
         uint32_t r[4];
         ldsm_x4_t(address(vbase, r_a, 2 * fp + c_a), r);
-        r[0] &= m0, r[1] &= m1, r[2] &= m0, r[3] &= m1;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          // bytes: (position 2 tig: features 2 gid, 2 gid + 1), (position 2 tig + 1: the same)
-          const uint32_t a[4] = {e4m3x2_to_half2(__byte_perm(r[2 * k], 0, 0x4420)),
-                                 e4m3x2_to_half2(__byte_perm(r[2 * k], 0, 0x4431)),
-                                 e4m3x2_to_half2(__byte_perm(r[2 * k + 1], 0, 0x4420)),
-                                 e4m3x2_to_half2(__byte_perm(r[2 * k + 1], 0, 0x4431))};
+          // bytes: position 2 tig, features 2 gid and 2 gid + 1; position 2 tig + 1, the same
+          uint32_t a[4];
+          e4m3x4_to_half2(__byte_perm(r[2 * k], 0, 0x3120), a[0], a[1]);
+          e4m3x4_to_half2(__byte_perm(r[2 * k + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_16816(o[2 * fp + k][nt], a, ph[nt][0], ph[nt][1]);
@@ -451,7 +493,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       for (int fb = 0; fb < DH / 16; ++fb) {
         uint32_t a[4];
         ldsm_x4_t(address(vbase, r_t, 2 * fb + c_t), a);
-        a[0] &= m0, a[1] &= m0, a[2] &= m1, a[3] &= m1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_16816(o[fb][nt], a, ph[nt][0], ph[nt][1]);
@@ -507,52 +548,41 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (int nt = 0; nt < NT; ++nt)
           dst[(fb * NT + nt) * 32 + lane] = make_float4(o[fb][nt][0], o[fb][nt][1], o[fb][nt][2], o[fb][nt][3]);
     };
-    auto add = [&](const float4* src) {
+    if (warp >= 2) put(merge + (warp - 2) * kVec);
+    named_bar_sync(1, 32 * kWarps);
+    if (warp < 2) {
 #pragma unroll
       for (int fb = 0; fb < DH / 16; ++fb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float4 v = src[(fb * NT + nt) * 32 + lane];
+          const float4 v = merge[warp * kVec + (fb * NT + nt) * 32 + lane];
           o[fb][nt][0] += v.x, o[fb][nt][1] += v.y, o[fb][nt][2] += v.z, o[fb][nt][3] += v.w;
         }
-    };
-    if (warp >= 2) put(merge + (warp - 2) * kVec);
+      put(merge + warp * kVec);
+    }
     named_bar_sync(1, 32 * kWarps);
-    if (warp < 2) add(merge + warp * kVec);
-    if (warp == 1) put(merge + kVec);
-    named_bar_sync(1, 32 * kWarps);
-    if (warp != 0) continue;
-    add(merge + kVec);
-    if (d.flags & (kOpenLeft | kOpenRight)) {
-      const int64_t slot = 2 * (int64_t)blockIdx.x + ((d.flags & kOpenLeft) ? 0 : 1);
-      put(p.part + slot * kVec);
-      if (gid == 0)
+    // every warp adds and stores a quarter of the features
+    const bool open = d.flags & (kOpenLeft | kOpenRight);
+    const int64_t slot = 2 * (int64_t)blockIdx.x + ((d.flags & kOpenLeft) ? 0 : 1);
+    const float vs = FP8 ? p.v_scale[d.head] : 1.f;
+    __half* dst = p.out + (int64_t)d.row * p.out_stride + (int64_t)d.head * p.G * DH;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h0 = 8 * nt + 2 * tig;
+      if (open && warp == 0 && gid == 0) {
+        p.ml[slot * 8 * NT + h0] = make_float2(mtop[nt][0], lsum[nt][0]);
+        p.ml[slot * 8 * NT + h0 + 1] = make_float2(mtop[nt][1], lsum[nt][1]);
+      }
+      const float i0 = lsum[nt][0] == 0.f ? 0.f : vs / lsum[nt][0];
+      const float i1 = lsum[nt][1] == 0.f ? 0.f : vs / lsum[nt][1];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            p.ml[slot * 8 * NT + 8 * nt + 2 * tig + e] = make_float2(mtop[nt][e], lsum[nt][e]);
-    } else {
-      const float vs = FP8 ? p.v_scale[d.head] : 1.f;
-      __half* dst = p.out + (int64_t)d.row * p.out_stride + (int64_t)d.head * p.G * DH;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int hd = 8 * nt + 2 * tig + e;
-          if (hd >= p.G) continue;
-          const float inv = lsum[nt][e] == 0.f ? 0.f : vs / lsum[nt][e];
-#pragma unroll
-          for (int fb = 0; fb < DH / 16; ++fb) {
-            if constexpr (FP8) {
-              *reinterpret_cast<__half2*>(dst + hd * DH + 16 * fb + 2 * gid) =
-                  __floats2half2_rn(o[fb][nt][e] * inv, o[fb][nt][2 + e] * inv);
-            } else {
-              dst[hd * DH + 16 * fb + gid] = __float2half_rn(o[fb][nt][e] * inv);
-              dst[hd * DH + 16 * fb + 8 + gid] = __float2half_rn(o[fb][nt][2 + e] * inv);
-            }
-          }
-        }
+      for (int b = 0; b < DH / 64; ++b) {
+        const int fb = warp * (DH / 64) + b, at = (fb * NT + nt) * 32 + lane;
+        const float4 u = merge[at], v = merge[kVec + at];
+        const float4 y = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+        if (open) p.part[slot * kVec + at] = y;
+        else store_out<DH, FP8>(dst, h0, p.G, 16 * fb, gid, y, i0, i1);
+      }
     }
   }
 }
@@ -612,15 +642,7 @@ paged_combine_kernel(const Params p) {
     acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
   }
   __half* dst = p.out + (int64_t)row * p.out_stride + (int64_t)head * p.G * DH;
-  const int f0 = 16 * fb + (FP8 ? 2 * gid : gid), f1 = 16 * fb + (FP8 ? 2 * gid + 1 : 8 + gid);
-  if (h0 < p.G) {
-    dst[h0 * DH + f0] = __float2half_rn(acc.x * inv[h0]);
-    dst[h0 * DH + f1] = __float2half_rn(acc.z * inv[h0]);
-  }
-  if (h0 + 1 < p.G) {
-    dst[(h0 + 1) * DH + f0] = __float2half_rn(acc.y * inv[h0 + 1]);
-    dst[(h0 + 1) * DH + f1] = __float2half_rn(acc.w * inv[h0 + 1]);
-  }
+  store_out<DH, FP8>(dst, h0, p.G, 16 * fb, gid, acc, inv[h0], inv[h0 + 1]);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn_p() {
