@@ -9,6 +9,9 @@
 //  * copy_pages_kernel: page src[i] of every pool to page dst[i].
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
+#include "sm100_ptx.cuh"
 #include "tri_internal.cuh"
 
 namespace tri {
@@ -59,9 +62,12 @@ struct AppendParams {
   void *k, *v;
   int64_t qkv_stride, q_stride, table_stride, page_stride, T, cs_rows;
   int H, Hkv, rot, pages, seqs, page_shift, max_pos;
-  int tokens_per_cta, head_step;
   float eps;
-  bool interleaved;
+  // of the many-row kernel: rows and heads of an item, chunks of heads per row,
+  // blocks of rows, steps of gridDim.x items, log2 of the groups of lanes per row
+  int rows, heads, chunks, next_chunk, gpt_shift, stage_bytes;
+  int64_t blocks, next_block;
+  unsigned* error;
 };
 
 __device__ __forceinline__ uint32_t h2_bits(float a, float b) {
@@ -69,147 +75,329 @@ __device__ __forceinline__ uint32_t h2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// eight fp32 values as fp16 (16 bytes) or as e4m3 of value / scale (8 bytes; the
-// IEEE quotient, so that the bytes are those of the plain definition)
+// Eight features of a head in fp32, as two fp32 pairs of four consecutive ones.
+// e4m3: value / scale (the IEEE quotient, so that the bytes are those of the
+// plain definition), clamped to +-448.
 template <bool FP8>
-__device__ __forceinline__ void store8(void* base, int64_t elem, const float (&y)[8], float scale) {
+__device__ __forceinline__ void store4(void* base, int64_t elem, const float* y, float scale) {
   if constexpr (FP8) {
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-          make_float2(__fdiv_rn(y[4 * h], scale), __fdiv_rn(y[4 * h + 1], scale)), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-          make_float2(__fdiv_rn(y[4 * h + 2], scale), __fdiv_rn(y[4 * h + 3], scale)), __NV_SATFINITE, __NV_E4M3);
-      w[h] = lo | (hi << 16);
-    }
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + elem) = make_uint2(w[0], w[1]);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[0], scale), __fdiv_rn(y[1], scale)),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[2], scale), __fdiv_rn(y[3], scale)),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(base) + elem) = lo | (hi << 16);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<__half*>(base) + elem) =
-        make_uint4(h2_bits(y[0], y[1]), h2_bits(y[2], y[3]), h2_bits(y[4], y[5]), h2_bits(y[6], y[7]));
+    *reinterpret_cast<uint2*>(static_cast<__half*>(base) + elem) = make_uint2(h2_bits(y[0], y[1]), h2_bits(y[2], y[3]));
   }
 }
 
-// A group of DH / 8 lanes owns one head: lane l holds features 8l .. 8l + 7
-// (one 16-byte load), the sum of squares is a shuffle reduction over the group,
-// and the partner of a rotate-half pair sits rot / 16 lanes away (rot is a
-// multiple of 16, so lanes rotate whole).  A group keeps its row's angles in
-// registers over all heads it takes, and has the loads of four heads in flight.
-template <int DH, bool FP8>
-__global__ void __launch_bounds__(256)
-paged_append_kernel(const AppendParams p) {
-  constexpr int LPH = DH / 8, GROUPS = 256 / LPH, U = 4;
-  const int lane = threadIdx.x & 31, l = threadIdx.x % LPH, grp = threadIdx.x / LPH;
-  const int gpt = GROUPS / p.tokens_per_cta;                    // groups per row
-  const int64_t t = (int64_t)blockIdx.x * p.tokens_per_cta + grp / gpt;
-  const int first = (int)blockIdx.y * gpt + grp % gpt;
-  const int nh = p.H + 2 * p.Hkv;
-  // the row's place; shuffles below need whole warps, so rows that do not
-  // exist stay and do nothing
-  int pp = -1, sq = -1, page = -1;
-  if (t < p.T) {
-    pp = p.pos[t];
-    sq = p.seq ? p.seq[t] : (t < p.seqs ? (int)t : -1);
-    if (pp < 0 || pp >= p.max_pos || pp >= p.cs_rows || sq < 0 || sq >= p.seqs) pp = -1;
+__device__ __forceinline__ void unpack4(uint2 raw, float* x) {
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&raw.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&raw.y));
+  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+
+// A group of DH / 8 lanes owns one head; a lane holds two runs of four features
+// such that both members of a rotated pair are its own: lane l with 4l < rot / 2
+// has pairs 4l .. 4l + 3, i.e. features 4l.. and rot/2 + 4l.. (rotate-half) or 8l..
+// and 8l + 4.. (interleaved); the lanes after those share the features from rot
+// on.  The sum of squares is a shuffle reduction over the group.  With the norm's
+// factor r the result is r (x_i (g_i c_i) + x_j (g_j s_i)), j the partner of i and
+// s_i its signed sine: the products of gain and angle are formed once per row and
+// kind of head.
+struct Eight {
+  uint2 lo, hi;
+};
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 mul2(float a0, float a1, float b0, float b1) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}" : "=f"(d.x), "=f"(d.y) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float a0, float a1, float b0, float b1, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+template <int DH, bool INTER>
+struct Turner {
+  static constexpr int LPH = DH / 8;
+  static constexpr int P = INTER ? 1 : 4;       // feature e's partner is e ^ P
+  float a[8], b[8];
+  int f0, f1;                                   // first features of the two runs
+  bool rotates, all;                            // this lane; every lane
+
+  __device__ explicit Turner(int rot) {
+    const int l = threadIdx.x % LPH;
+    all = rot == DH;
+    rotates = 4 * l < rot / 2;
+    f0 = INTER || !rotates ? 8 * l : 4 * l;     // past the rotated ones: rot + 2 (4l - rot / 2) = 8l
+    f1 = INTER || !rotates ? 8 * l + 4 : rot / 2 + 4 * l;
   }
-  const bool valid = pp >= 0;
-  if (valid) {
-    page = p.table[(int64_t)sq * p.table_stride + (pp >> p.page_shift)];
-    if (page >= p.pages) page = -1;
+  __device__ __forceinline__ Eight load(const __half* head) const {
+    return {*reinterpret_cast<const uint2*>(head + f0), *reinterpret_cast<const uint2*>(head + f1)};
   }
-  // angles: c and the signed s of own features (the partner's share of each)
-  const int hl = p.rot / 16;                                    // lanes of half the rotated features
-  const bool rotates = 8 * l < p.rot;
-  float c[8], s[8];
+  // angles: the row's (cos, sin) pairs; gains: or null
+  __device__ __forceinline__ void coefficients(const __half* gains, const float4* angles) {
+    float g[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
-  int partner = lane;
-  if (rotates && valid) {
-    const float4* row = reinterpret_cast<const float4*>(p.cs + (int64_t)pp * p.rot);
-    if (p.interleaved) {
+    for (int e = 0; e < 8; ++e) g[e] = 1.f;
+    if (gains) {
+      const Eight r = load(gains);
+      unpack4(r.lo, g);
+      unpack4(r.hi, g + 4);
+    }
+    if (!rotates) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 w = row[2 * l + e];                        // pairs 4l + 2e, 4l + 2e + 1
-        c[4 * e] = c[4 * e + 1] = w.x, s[4 * e] = -w.y, s[4 * e + 1] = w.y;
-        c[4 * e + 2] = c[4 * e + 3] = w.z, s[4 * e + 2] = -w.w, s[4 * e + 3] = w.w;
+      for (int e = 0; e < 8; ++e) a[e] = g[e], b[e] = 0.f;
+      return;
+    }
+    const int l = threadIdx.x % LPH;
+    const float4 w0 = angles[2 * l], w1 = angles[2 * l + 1];    // pairs 4l .. 4l + 3
+    const float c[4] = {w0.x, w0.z, w1.x, w1.z}, s[4] = {w0.y, w0.w, w1.y, w1.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = INTER ? 2 * i : i, y = x ^ P;
+      a[x] = g[x] * c[i], b[x] = -g[y] * s[i];
+      a[y] = g[y] * c[i], b[y] = g[x] * s[i];
+    }
+  }
+  // a head's eight features, normed and turned; every lane of the warp calls it
+  __device__ __forceinline__ void turn(const Eight& r, bool norm, float eps, float (&y)[8]) const {
+    float x[8];
+    unpack4(r.lo, x);
+    unpack4(r.hi, x + 4);
+    float rstd = 1.f;
+    if (norm) {
+      float2 s2 = mul2(x[0], x[1], x[0], x[1]);
+#pragma unroll
+      for (int e = 2; e < 8; e += 2) s2 = fma2(x[e], x[e + 1], x[e], x[e + 1], s2);
+      float ss = s2.x + s2.y;
+#pragma unroll
+      for (int d = LPH / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+      rstd = rsqrtf(fmaf(ss, 1.f / (float)DH, eps));            // a few units of 2^-24
+    }
+    if (all) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 own = mul2(x[e], x[e + 1], a[e], a[e + 1]);
+        const float2 v = fma2(x[e ^ P], x[(e + 1) ^ P], b[e], b[e + 1], own);
+        const float2 w = mul2(v.x, v.y, rstd, rstd);
+        y[e] = w.x, y[e + 1] = w.y;
       }
     } else {
-      const int lo = l < hl ? l : l - hl;
-      const float sg = l < hl ? -1.f : 1.f;
+      // lanes that do not rotate leave the partner out: its b is 0, and 0 x Inf would not be
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 w = row[4 * lo + e];
-        c[2 * e] = w.x, s[2 * e] = sg * w.y, c[2 * e + 1] = w.z, s[2 * e + 1] = sg * w.w;
-      }
+      for (int e = 0; e < 8; ++e) y[e] = (rotates ? fmaf(x[e ^ P], b[e], x[e] * a[e]) : x[e] * a[e]) * rstd;
     }
   }
-  if (rotates && !p.interleaved) partner = l < hl ? lane + hl : lane - hl;
-  uint4 gq = make_uint4(0, 0, 0, 0), gk = gq;
-  if (p.gq) {
-    gq = reinterpret_cast<const uint4*>(p.gq)[l];
-    gk = reinterpret_cast<const uint4*>(p.gk)[l];
+  template <bool FP8>
+  __device__ __forceinline__ void store(void* base, int64_t head, const float (&y)[8], float scale) const {
+    store4<FP8>(base, head + f0, y, scale);
+    store4<FP8>(base, head + f1, y + 4, scale);
   }
-  const __half* src = p.qkv + t * p.qkv_stride;
-  const int off = pp & ((1 << p.page_shift) - 1);
-  for (int b = 0; b < nh; b += U * p.head_step) {
-    uint4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = b + u * p.head_step + first;
-      raw[u] = valid && j < nh ? __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)j * DH) + l)
-                               : make_uint4(0, 0, 0, 0);
+};
+
+// row t's position (-1: it writes nothing) and sequence
+__device__ __forceinline__ int row_position(const AppendParams& p, int64_t t, int& sq) {
+  const int pp = p.pos[t];
+  sq = p.seq ? p.seq[t] : (t < p.seqs ? (int)t : -1);
+  return pp < p.max_pos && pp < p.cs_rows && sq >= 0 && sq < p.seqs && pp >= 0 ? pp : -1;
+}
+__device__ __forceinline__ int row_page(const AppendParams& p, int pp, int sq) {
+  const int page = p.table[(int64_t)sq * p.table_stride + (pp >> p.page_shift)];
+  return page < p.pages ? page : -1;
+}
+
+// key (or value) head kv of a row into its page
+template <int DH, bool FP8, bool INTER>
+__device__ __forceinline__ void store_kv(const AppendParams& p, const Turner<DH, INTER>& tn, int page, int pp, int kv,
+                                         bool is_v, const Eight& raw, float (&y)[8]) {
+  const int64_t at = (int64_t)page * p.page_stride +
+                     (((int64_t)kv << p.page_shift) + (pp & ((1 << p.page_shift) - 1))) * DH;
+  if (is_v && !FP8) {                                           // as given, bit for bit
+    __half* dst = static_cast<__half*>(p.v) + at;
+    *reinterpret_cast<uint2*>(dst + tn.f0) = raw.lo;
+    *reinterpret_cast<uint2*>(dst + tn.f1) = raw.hi;
+    return;
+  }
+  if (is_v) {
+    unpack4(raw.lo, y);
+    unpack4(raw.hi, y + 4);
+  }
+  tn.template store<FP8>(is_v ? p.v : p.k, at, y, FP8 ? (is_v ? p.v_scale : p.k_scale)[kv] : 1.f);
+}
+
+// Few rows: one head per group, spread over the CTAs, every load issued at once.
+template <int DH, bool FP8, bool INTER>
+__global__ void __launch_bounds__(256)
+paged_append_kernel(const AppendParams p) {
+  constexpr int LPH = DH / 8, GROUPS = 256 / LPH;
+  const int64_t t = blockIdx.x;
+  const int j = (int)blockIdx.y * GROUPS + threadIdx.x / LPH;
+  const bool exists = j < p.H + 2 * p.Hkv;
+  Turner<DH, INTER> tn(p.rot);
+  Eight raw = {};
+  if (exists) raw = tn.load(p.qkv + t * p.qkv_stride + (int64_t)j * DH);
+  int sq;
+  const int pp = row_position(p, t, sq);
+  if (pp < 0) return;                                           // the whole CTA: it has one row
+  const int page = row_page(p, pp, sq);
+  tn.coefficients(j < p.H ? p.gq : p.gk, reinterpret_cast<const float4*>(p.cs + (int64_t)pp * p.rot));
+  float y[8];
+  tn.turn(raw, p.gq, p.eps, y);
+  if (!exists) return;
+  if (j < p.H) {
+    tn.template store<false>(p.q_out, t * p.q_stride + (int64_t)j * DH, y, 1.f);
+  } else if (page >= 0) {
+    const int kv = j - p.H;
+    store_kv<DH, FP8>(p, tn, page, pp, kv < p.Hkv ? kv : kv - p.Hkv, kv >= p.Hkv, raw, y);
+  }
+}
+
+// Many rows: persistent CTAs.  An item is `rows` consecutive rows (all heads), or
+// a run of one row's heads where a row is long; about 20 KB.  The producer warp
+// looks the rows up an item ahead (a lane per row) and bulk-copies them and
+// their angles into a ring of stages, so that every load's latency is behind
+// the items before it; eight warps turn and store.
+constexpr int kFewCtasPerSm = 4;
+constexpr int kItemBytes = 20 * 1024 + 512;
+constexpr int kAppendStages = 3;
+constexpr int kAppendThreads = 288;
+constexpr uint32_t kWaitPolls = 1u << 18;                       // about a second
+constexpr unsigned kAppendProducerCode = 61, kAppendConsumerCode = 62, kAppendDrainCode = 63;
+
+// the items of a CTA: block (of rows) and chunk (of heads), gridDim.x apart
+struct Item {
+  int64_t block;
+  int chunk;
+  __device__ explicit Item(const AppendParams& p)
+      : block(blockIdx.x / p.chunks), chunk((int)(blockIdx.x % p.chunks)) {}
+  __device__ void next(const AppendParams& p) {
+    block += p.next_block;
+    chunk += p.next_chunk;
+    if (chunk >= p.chunks) chunk -= p.chunks, ++block;
+  }
+};
+
+template <int DH, bool FP8, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads, 3)
+paged_append_stream_kernel(const AppendParams p) {
+  using namespace ptx;
+  constexpr int LPH = DH / 8, GROUPS = 256 / LPH;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ uint64_t full[kAppendStages], empty[kAppendStages];
+  __shared__ int2 place[kAppendStages][32];                     // (position or -1, page or -1) of the item's rows
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kAppendStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 8);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (b + u * p.head_step >= nh) break;                     // the same for every lane
-      const int j = b + u * p.head_step + first;
-      float y[8];
-      const __half2* h = reinterpret_cast<const __half2*>(&raw[u]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(h[e]);
-        y[2 * e] = f.x, y[2 * e + 1] = f.y;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int nh = p.H + 2 * p.Hkv;
+  uint32_t polls = kWaitPolls;
+  int st = 0;
+  if (warp == 8) {
+    uint32_t phase = 1;
+    int64_t n = 0;
+    auto look = [&](const Item& it, int& sq) -> int {
+      const int64_t t = it.block * p.rows + lane;
+      return lane < p.rows && t < p.T ? row_position(p, t, sq) : -1;
+    };
+    int sq = 0, sq_next = 0;
+    Item item(p), item2(p);
+    int pp = look(item, sq);
+    int page = pp >= 0 ? row_page(p, pp, sq) : -1;
+    item2.next(p);
+    int pp_next = look(item2, sq_next);
+    item2.next(p);
+    for (; item.block < p.blocks; item.next(p), item2.next(p), ++n, ++st) {
+      if (st == kAppendStages) st = 0, phase ^= 1;
+      const int page_next = pp_next >= 0 ? row_page(p, pp_next, sq_next) : -1;
+      int sq2 = 0;
+      const int pp2 = look(item2, sq2);
+      if (n >= kAppendStages && !mbar_wait(&empty[st], phase, polls)) {
+        if (lane == 0) record_wait_failure(p.error, kAppendProducerCode);
+        polls = 1;
       }
-      const bool is_v = j >= p.H + p.Hkv;
-      if (p.gq) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (!is_v) {
-          const float rstd = 1.f / sqrtf(ss / (float)DH + p.eps);
-          const __half2* g = reinterpret_cast<const __half2*>(j < p.H ? &gq : &gk);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(g[e]);
-            y[2 * e] *= rstd * f.x, y[2 * e + 1] *= rstd * f.y;
-          }
+      const int h0 = item.chunk * p.heads, nhc = nh - h0 < p.heads ? nh - h0 : p.heads;
+      place[st][lane] = make_int2(pp, page);
+      const int live = __popc(__ballot_sync(0xFFFFFFFFu, pp >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(live * (nhc * DH * 2 + p.rot * 4)));
+      __syncwarp();
+      if (pp >= 0) {
+        uint8_t* dst = sm + st * p.stage_bytes;
+        bulk_load(dst + lane * p.heads * DH * 2, p.qkv + (item.block * p.rows + lane) * p.qkv_stride + (int64_t)h0 * DH,
+                  (uint32_t)(nhc * DH * 2), &full[st]);
+        bulk_load(dst + p.rows * p.heads * DH * 2 + lane * p.rot * 4, p.cs + (int64_t)pp * p.rot,
+                  (uint32_t)(p.rot * 4), &full[st]);
+      }
+      pp = pp_next, page = page_next, pp_next = pp2, sq_next = sq2;
+    }
+    // every copy has landed before the CTA may leave
+    for (int64_t i = n > kAppendStages ? n - kAppendStages : 0; i < n; ++i)
+      if (!mbar_wait(&full[i % kAppendStages], (uint32_t)(i / kAppendStages) & 1, kWaitPolls) && lane == 0)
+        record_wait_failure(p.error, kAppendDrainCode);
+    return;
+  }
+  const int grp = threadIdx.x / LPH, gi = grp & ((1 << p.gpt_shift) - 1), gr = grp >> p.gpt_shift;
+  const int gpt = 1 << p.gpt_shift, per_pass = GROUPS >> p.gpt_shift;
+  Turner<DH, INTER> tn(p.rot);
+  uint32_t phase = 0;
+  for (Item item(p); item.block < p.blocks; item.next(p), ++st) {
+    if (st == kAppendStages) st = 0, phase ^= 1;
+    if (!mbar_wait(&full[st], phase, polls)) {
+      if (lane == 0) record_wait_failure(p.error, kAppendConsumerCode);
+      polls = 1;
+    }
+    __syncwarp();
+    const int64_t t0 = item.block * p.rows;
+    const int h0 = item.chunk * p.heads, nhc = nh - h0 < p.heads ? nh - h0 : p.heads;
+    const int nq = p.H - h0 < 0 ? 0 : (p.H - h0 < nhc ? p.H - h0 : nhc), nkv = nhc - nq;
+    // the keys and values go to the groups that follow those of the last queries
+    const int gkv = (gi - nq) & (gpt - 1);
+    const uint8_t* stage = sm + st * p.stage_bytes;
+    for (int r0 = 0; r0 < p.rows; r0 += per_pass) {             // shuffles below: trip counts are the CTA's
+      const bool real = r0 + gr < p.rows;
+      const int r = real ? r0 + gr : p.rows - 1;
+      const int2 at = place[st][r];
+      const bool valid = real && at.x >= 0;
+      const __half* src = reinterpret_cast<const __half*>(stage) + r * p.heads * DH;
+      const float4* angles = reinterpret_cast<const float4*>(stage + p.rows * p.heads * DH * 2 + r * p.rot * 4);
+      if (nq > 0) {
+        tn.coefficients(p.gq, angles);
+        __half* dst = p.q_out + (t0 + r) * p.q_stride + (int64_t)h0 * DH;
+#pragma unroll 1
+        for (int j0 = 0; j0 < nq; j0 += gpt) {
+          const int j = j0 + gi;
+          float y[8];
+          tn.turn(tn.load(src + (j < nq ? j : 0) * DH), p.gq, p.eps, y);
+          if (valid && j < nq) tn.template store<false>(dst, j * DH, y, 1.f);
         }
       }
-      float o[8];
-      if (p.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = y[e ^ 1];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xFFFFFFFFu, y[e], partner);
-      }
-      if (!is_v && rotates) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], c[e], o[e] * s[e]);
-      }
-      if (!valid || j >= nh) continue;
-      if (j < p.H) {
-        store8<false>(p.q_out, t * p.q_stride + (int64_t)j * DH + 8 * l, y, 1.f);
-      } else if (page >= 0) {
-        const int kv = is_v ? j - p.H - p.Hkv : j - p.H;
-        const int64_t at =
-            (int64_t)page * p.page_stride + ((((int64_t)kv << p.page_shift) + off) * DH) + 8 * l;
-        const float scale = FP8 ? (is_v ? p.v_scale : p.k_scale)[kv] : 1.f;
-        store8<FP8>(is_v ? p.v : p.k, at, y, scale);
+      if (nkv > 0) {
+        tn.coefficients(p.gk, angles);
+        for (int j0 = 0; j0 < nkv; j0 += gpt) {
+          const int j = j0 + gkv;
+          const Eight raw = tn.load(src + (nq + (j < nkv ? j : 0)) * DH);
+          float y[8];
+          tn.turn(raw, p.gq, p.eps, y);
+          const int kv = h0 + nq + j - p.H;
+          if (valid && j < nkv && at.y >= 0)
+            store_kv<DH, FP8>(p, tn, at.y, at.x, kv < p.Hkv ? kv : kv - p.Hkv, kv >= p.Hkv, raw, y);
+        }
       }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
   }
 }
 
@@ -280,31 +468,56 @@ cudaError_t launch_paged_qknorm_rope(const __half* qkv, int64_t qkv_stride, cons
   p.qkv_stride = qkv_stride, p.q_stride = q_stride, p.table_stride = c.table_stride;
   p.page_stride = c.page_stride, p.T = T, p.cs_rows = cs_rows;
   p.H = (int)H, p.Hkv = (int)c.heads, p.rot = (int)rot, p.pages = (int)c.pages;
-  p.seqs = (int)c.seqs, p.max_pos = (int)(c.seq_pages * c.page_size), p.eps = eps, p.interleaved = interleaved;
+  p.seqs = (int)c.seqs, p.max_pos = (int)(c.seq_pages * c.page_size), p.eps = eps;
   while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
-  // Few rows: one head per group and the heads spread over CTAs (latency);
-  // many: a row per as many groups as give each about four heads, so that the
-  // row's lookups and angles are paid once and four loads are in flight.
   const int groups = (int)(256 * 8 / c.head_dim);
-  const int64_t nh = H + 2 * c.heads;
-  int gpt = 1;
-  while (gpt < groups && gpt * 4 < nh) gpt *= 2;
-  int64_t splits = 1;
-  if (T * ceil_div(nh, groups) <= 2 * (int64_t)sms) {
-    gpt = groups;
-    splits = ceil_div(nh, groups);
+  const int64_t nh = H + 2 * c.heads, head_bytes = c.head_dim * 2;
+  const bool fp8 = c.dtype == TRI_CACHE_E4M3;
+  using D128 = std::integral_constant<int, 128>;
+  using D64 = std::integral_constant<int, 64>;
+  auto pick = [&](auto run) -> cudaError_t {
+    if (c.head_dim == 128) {
+      if (fp8) return interleaved ? run(D128{}, std::true_type{}, std::true_type{}) : run(D128{}, std::true_type{}, std::false_type{});
+      return interleaved ? run(D128{}, std::false_type{}, std::true_type{}) : run(D128{}, std::false_type{}, std::false_type{});
+    }
+    if (fp8) return interleaved ? run(D64{}, std::true_type{}, std::true_type{}) : run(D64{}, std::true_type{}, std::false_type{});
+    return interleaved ? run(D64{}, std::false_type{}, std::true_type{}) : run(D64{}, std::false_type{}, std::false_type{});
+  };
+  if (T * ceil_div(nh, groups) <= kFewCtasPerSm * (int64_t)sms) {
+    const dim3 grid((unsigned)T, (unsigned)ceil_div(nh, groups));
+    return pick([&](auto dh, auto e, auto il) -> cudaError_t {
+      paged_append_kernel<decltype(dh)::value, decltype(e)::value, decltype(il)::value><<<grid, 256, 0, s>>>(p);
+      return cudaGetLastError();
+    });
   }
-  p.tokens_per_cta = groups / gpt;
-  p.head_step = (int)(gpt * splits);
-  const dim3 grid((unsigned)ceil_div(T, p.tokens_per_cta), (unsigned)splits);
-  if (c.dtype == TRI_CACHE_E4M3) {
-    if (c.head_dim == 128) paged_append_kernel<128, true><<<grid, 256, 0, s>>>(p);
-    else paged_append_kernel<64, true><<<grid, 256, 0, s>>>(p);
-  } else {
-    if (c.head_dim == 128) paged_append_kernel<128, false><<<grid, 256, 0, s>>>(p);
-    else paged_append_kernel<64, false><<<grid, 256, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  const int64_t row_bytes = nh * head_bytes + rot * 4;
+  p.rows = row_bytes >= kItemBytes ? 1 : (int)(kItemBytes / row_bytes < 32 ? kItemBytes / row_bytes : 32);
+  p.heads = (int)(nh <= kItemBytes / head_bytes ? nh : kItemBytes / head_bytes);
+  p.chunks = (int)ceil_div(nh, p.heads);
+  p.blocks = ceil_div(T, p.rows);
+  p.stage_bytes = (int)((p.rows * (p.heads * head_bytes + rot * 4) + 127) & ~int64_t(127));
+  // about four heads per group of lanes, and no group without a row
+  while ((1 << p.gpt_shift) < groups && ((4 << p.gpt_shift) < p.heads || (groups >> p.gpt_shift) > p.rows)) ++p.gpt_shift;
+  const int64_t items = p.blocks * p.chunks, most = 3 * (int64_t)sms;
+  const int ctas = (int)(items < most ? items : most);
+  p.next_block = ctas / p.chunks, p.next_chunk = ctas % p.chunks;
+  cudaError_t err = wait_status_word(&p.error);
+  if (err != cudaSuccess) return err;
+  const int smem = kAppendStages * p.stage_bytes;
+  return pick([&](auto dh, auto e, auto il) -> cudaError_t {
+    auto kernel = paged_append_stream_kernel<decltype(dh)::value, decltype(e)::value, decltype(il)::value>;
+    static bool ready[64] = {};
+    int dev = 0;
+    cudaError_t r = cudaGetDevice(&dev);
+    if (r != cudaSuccess) return r;
+    if (dev >= 64 || !ready[dev]) {
+      r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendStages * (kItemBytes + 1024));
+      if (r != cudaSuccess) return r;
+      if (dev < 64) ready[dev] = true;
+    }
+    kernel<<<(unsigned)ctas, kAppendThreads, smem, s>>>(p);
+    return cudaGetLastError();
+  });
 }
 
 cudaError_t launch_copy_pages(uint8_t* pools, int64_t n_pools, int64_t pool_stride, int64_t pages,

@@ -72,11 +72,12 @@ def norm_rotate_f64(x, gain, cs_row, interleaved: bool, eps: float = 1e-5) -> np
     x = np.array(x, dtype=np.float64)
     if gain is not None:
         x = x / math.sqrt(float(np.mean(x * x)) + eps) * np.asarray(gain, np.float64)
-    rot = 2 * len(cs_row)
+    half = len(cs_row)
+    i = np.arange(half)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+    c, s = np.asarray(cs_row, np.float64).T
     y = x.copy()
-    for i, (c, s) in enumerate(np.asarray(cs_row, np.float64)):
-        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
-        y[a], y[b] = x[a] * c - x[b] * s, x[b] * c + x[a] * s
+    y[a], y[b] = x[a] * c - x[b] * s, x[b] * c + x[a] * s
     return y
 
 

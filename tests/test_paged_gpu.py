@@ -155,6 +155,10 @@ def _check_append(T, H, Hkv, dh, ps, rot, inter, norm, fp8, seed, S=None, wide=0
     (37, 5, 1, 64, 8, 64, True, 4),
     (130, 12, 12, 128, 16, 96, False, 7),
     (700, 4, 2, 64, 32, 32, True, 5),
+    (1201, 1, 1, 64, 8, 16, False, 40),      # 32 rows an item, the last one ragged
+    (640, 3, 3, 128, 16, 80, True, 9),
+    (301, 90, 10, 128, 64, 128, False, 3),   # a row longer than an item: two runs of heads
+    (333, 60, 60, 64, 32, 64, True, 2),
 ])
 def test_append(T, H, Hkv, dh, ps, rot, inter, S, norm, fp8):
     _check_append(T, H, Hkv, dh, ps, rot, inter, norm, fp8, T + H + rot, S)
