@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -36,10 +37,13 @@ ROPE_KINDS = {"linear": 1, "ntk": 2, "bands": 3, "ramp": 4}
 
 
 class PagedCacheDesc(ctypes.Structure):
-    """tri_paged_cache."""
+    """tri_paged_cache (wrappers pack the same bytes with PAGED_CACHE)."""
     _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("table", _p),
                 ("pages", _i64), ("page_size", _i64), ("page_stride", _i64), ("heads", _i64), ("head_dim", _i64),
                 ("seqs", _i64), ("seq_pages", _i64), ("table_stride", _i64), ("dtype", ctypes.c_int32)]
+
+
+PAGED_CACHE = struct.Struct("PPPPPqqqqqqqqi4x")
 
 
 class RopeScaling(ctypes.Structure):
@@ -74,11 +78,11 @@ SIGNATURES = {
     "tri_qknorm_rope": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _f, _p]),
     "tri_attention_decode_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "tri_attention_decode": (_i, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _p, _sz, _p]),
-    "tri_rope_table_scaled": (_i, [_p, _i64, _i64, ctypes.c_double, ctypes.POINTER(RopeScaling), _p]),
+    "tri_rope_table_scaled": (_i, [_p, _i64, _i64, ctypes.c_double, _p, _p]),
     "tri_paged_qknorm_rope": (_i, [_p, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i, _p, _i64,
-                                   ctypes.POINTER(PagedCacheDesc), _i64, _i64, _f, _p]),
+                                   _p, _i64, _i64, _f, _p]),
     "tri_paged_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
-    "tri_paged_attention": (_i, [_p, _i64, _p, _p, ctypes.POINTER(PagedCacheDesc), _p, _i64, _i64, _i64, _f, _p, _sz,
+    "tri_paged_attention": (_i, [_p, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _f, _p, _sz,
                                  _p]),
     "tri_copy_pages": (_i, [_p, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _p]),
 }

@@ -214,23 +214,25 @@ __device__ __forceinline__ int row_page(const AppendParams& p, int pp, int sq) {
   return page < p.pages ? page : -1;
 }
 
-// key (or value) head kv of a row into its page
+// where element 0 of head 0 of a row's page slot lies
+__device__ __forceinline__ int64_t row_place(const AppendParams& p, int page, int pp, int dh) {
+  return (int64_t)page * p.page_stride + (int64_t)(pp & ((1 << p.page_shift) - 1)) * dh;
+}
+// value head kv of a row: as given (bit for bit), or in e4m3
 template <int DH, bool FP8, bool INTER>
-__device__ __forceinline__ void store_kv(const AppendParams& p, const Turner<DH, INTER>& tn, int page, int pp, int kv,
-                                         bool is_v, const Eight& raw, float (&y)[8]) {
-  const int64_t at = (int64_t)page * p.page_stride +
-                     (((int64_t)kv << p.page_shift) + (pp & ((1 << p.page_shift) - 1))) * DH;
-  if (is_v && !FP8) {                                           // as given, bit for bit
+__device__ __forceinline__ void store_value(const AppendParams& p, const Turner<DH, INTER>& tn, int64_t place, int kv,
+                                            const Eight& raw) {
+  const int64_t at = place + ((int64_t)kv << p.page_shift) * DH;
+  if constexpr (FP8) {
+    float y[8];
+    unpack4(raw.lo, y);
+    unpack4(raw.hi, y + 4);
+    tn.template store<true>(p.v, at, y, p.v_scale[kv]);
+  } else {
     __half* dst = static_cast<__half*>(p.v) + at;
     *reinterpret_cast<uint2*>(dst + tn.f0) = raw.lo;
     *reinterpret_cast<uint2*>(dst + tn.f1) = raw.hi;
-    return;
   }
-  if (is_v) {
-    unpack4(raw.lo, y);
-    unpack4(raw.hi, y + 4);
-  }
-  tn.template store<FP8>(is_v ? p.v : p.k, at, y, FP8 ? (is_v ? p.v_scale : p.k_scale)[kv] : 1.f);
 }
 
 // Few rows: one head per group, spread over the CTAs, every load issued at once.
@@ -256,18 +258,22 @@ paged_append_kernel(const AppendParams p) {
     tn.template store<false>(p.q_out, t * p.q_stride + (int64_t)j * DH, y, 1.f);
   } else if (page >= 0) {
     const int kv = j - p.H;
-    store_kv<DH, FP8>(p, tn, page, pp, kv < p.Hkv ? kv : kv - p.Hkv, kv >= p.Hkv, raw, y);
+    const int64_t place = row_place(p, page, pp, DH);
+    if (kv < p.Hkv)
+      tn.template store<FP8>(p.k, place + ((int64_t)kv << p.page_shift) * DH, y, FP8 ? p.k_scale[kv] : 1.f);
+    else
+      store_value<DH, FP8>(p, tn, place, kv - p.Hkv, raw);
   }
 }
 
 // Many rows: persistent CTAs.  An item is `rows` consecutive rows (all heads), or
-// a run of one row's heads where a row is long; about 20 KB.  The producer warp
+// a run of one row's heads where a row is long; up to 25 KB.  The producer warp
 // looks the rows up an item ahead (a lane per row) and bulk-copies them and
 // their angles into a ring of stages, so that every load's latency is behind
 // the items before it; eight warps turn and store.
 constexpr int kFewCtasPerSm = 4;
-constexpr int kItemBytes = 20 * 1024 + 512;
-constexpr int kAppendStages = 3;
+constexpr int kItemBytes = 25 * 1024 + 512;
+constexpr int kAppendStages = 2;
 constexpr int kAppendThreads = 288;
 constexpr uint32_t kWaitPolls = 1u << 18;                       // about a second
 constexpr unsigned kAppendProducerCode = 61, kAppendConsumerCode = 62, kAppendDrainCode = 63;
@@ -361,9 +367,11 @@ paged_append_stream_kernel(const AppendParams p) {
     __syncwarp();
     const int64_t t0 = item.block * p.rows;
     const int h0 = item.chunk * p.heads, nhc = nh - h0 < p.heads ? nh - h0 : p.heads;
-    const int nq = p.H - h0 < 0 ? 0 : (p.H - h0 < nhc ? p.H - h0 : nhc), nkv = nhc - nq;
-    // the keys and values go to the groups that follow those of the last queries
-    const int gkv = (gi - nq) & (gpt - 1);
+    // of the item's heads, h0 .. h0 + nhc - 1: queries, keys, values
+    auto below = [&](int end) { return end - h0 < 0 ? 0 : (end - h0 < nhc ? end - h0 : nhc); };
+    const int nq = below(p.H), nqk = below(p.H + p.Hkv);
+    // keys follow on from the groups that had the last queries, values from theirs
+    const int gk = nq + ((gi - nq) & (gpt - 1)), gv = nqk + ((gi - nqk) & (gpt - 1));
     const uint8_t* stage = sm + st * p.stage_bytes;
     for (int r0 = 0; r0 < p.rows; r0 += per_pass) {             // shuffles below: trip counts are the CTA's
       const bool real = r0 + gr < p.rows;
@@ -383,18 +391,23 @@ paged_append_stream_kernel(const AppendParams p) {
           if (valid && j < nq) tn.template store<false>(dst, j * DH, y, 1.f);
         }
       }
-      if (nkv > 0) {
+      const int64_t place_kv = row_place(p, at.y, at.x, DH);
+      if (__any_sync(0xFFFFFFFFu, gk < nqk)) {
         tn.coefficients(p.gk, angles);
-        for (int j0 = 0; j0 < nkv; j0 += gpt) {
-          const int j = j0 + gkv;
-          const Eight raw = tn.load(src + (nq + (j < nkv ? j : 0)) * DH);
+        for (int j0 = 0; j0 < nqk - nq; j0 += gpt) {
+          const int j = j0 + gk;
+          if (!__any_sync(0xFFFFFFFFu, j < nqk)) break;
           float y[8];
-          tn.turn(raw, p.gq, p.eps, y);
-          const int kv = h0 + nq + j - p.H;
-          if (valid && j < nkv && at.y >= 0)
-            store_kv<DH, FP8>(p, tn, at.y, at.x, kv < p.Hkv ? kv : kv - p.Hkv, kv >= p.Hkv, raw, y);
+          tn.turn(tn.load(src + (j < nqk ? j : 0) * DH), p.gq, p.eps, y);
+          const int kv = h0 + j - p.H;
+          if (valid && j < nqk && at.y >= 0)
+            tn.template store<FP8>(p.k, place_kv + ((int64_t)kv << p.page_shift) * DH, y, FP8 ? p.k_scale[kv] : 1.f);
         }
       }
+      if (valid && at.y >= 0)
+        for (int j = gv; j < nhc; j += gpt)
+          store_value<DH, FP8>(p, tn, place_kv, h0 + j - p.H - p.Hkv, tn.load(src + j * DH));
+      __syncwarp();
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);

@@ -18,12 +18,11 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import math
 
 import torch
 
 from . import _lib
-from .api import Workspace, _ptr, _stream
+from .api import Workspace
 
 RMS_EPS = 1e-5
 ROPE_THETA = 5.0e5
@@ -31,62 +30,76 @@ E4M3 = torch.float8_e4m3fn
 _NULL = contextlib.nullcontext()
 
 
-def _on(device):
+# A decode step makes these calls for every block and token, so the checks are
+# kept to attribute reads: device indexes rather than device objects, one packed
+# struct rather than a ctypes one.
+_pack = _lib.PAGED_CACHE.pack
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_FP16, _I32, _F32 = torch.float16, torch.int32, torch.float32
+
+
+def _on(index: int):
     """The device as the current one (the library launches on the current device)."""
-    return _NULL if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _NULL if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _rows(t, width, name):
-    """(pointer, row stride) of a fp16 tensor whose rows of `width` elements are contiguous."""
-    if t.dtype != torch.float16:
+def _device(first, *ts) -> int:
+    """The index of the CUDA device that all the tensors live on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    for t in ts:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors must live on one CUDA device")
+    return index
+
+
+def _row_stride(t, rows, width, name) -> int:
+    """The row stride of a fp16 tensor of `rows` rows, each of `width` contiguous elements."""
+    st, sh = t.stride(), t.shape
+    if t.dtype != _FP16:
         raise ValueError(f"{name} must be float16")
-    n = t.shape[0]
-    if t.numel() != n * width or not (t[0].is_contiguous() if t.dim() > 2 else t.stride(1) == 1):
-        raise ValueError(f"{name} must hold rows of {width} contiguous elements")
-    return t.data_ptr(), (t.stride(0) if n > 1 else width)
+    if sh[0] != rows or not ((len(sh) == 2 and sh[1] == width and st[1] == 1) or
+                             (len(sh) == 3 and sh[1] * sh[2] == width and st[2] == 1 and
+                              (st[1] == sh[2] or sh[1] == 1))):
+        raise ValueError(f"{name} must hold {rows} rows of {width} contiguous elements")
+    return st[0] if rows > 1 else width
 
 
-def _int32(t, n, name):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+def _int32(t, n, name) -> int:
+    if t.dtype != _I32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor with one element per row")
     return t.data_ptr()
 
 
-def _desc(k, v, table, k_scale, v_scale, device):
-    """tri_paged_cache of two pools, a table and the scales."""
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+def _scale(s, heads) -> int:
+    if s is None or s.dtype != _F32 or s.shape != (heads,) or not s.is_contiguous():
+        raise ValueError("an e4m3 cache needs k_scale and v_scale, float32 [kv heads]")
+    return s.data_ptr()
+
+
+def _cache(k, v, table, k_scale, v_scale):
+    """(tri_paged_cache as bytes, kv heads, head dim) of two pools, a table and the scales."""
+    shape, st, dtype = k.shape, k.stride(), k.dtype
+    if len(shape) != 4 or v.shape != shape or v.stride() != st or v.dtype != dtype:
         raise ValueError("k and v must be alike: [pages][kv heads][page size][head dim]")
-    pages, heads, size, dh = k.shape
-    if k.stride()[1:] != (size * dh, dh, 1):
+    pages, heads, size, dh = shape
+    if st[3] != 1 or st[2] != dh or (st[1] != size * dh and heads > 1):
         raise ValueError("the heads of a page must be contiguous")
-    if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1:
+    tsh, tst = table.shape, table.stride()
+    if table.dtype != _I32 or len(tsh) != 2 or tst[1] != 1:
         raise ValueError("the page table must be int32 [sequences][pages] with contiguous rows")
-    if k.dtype == E4M3:
-        if k_scale is None or v_scale is None:
-            raise ValueError("an e4m3 cache needs k_scale and v_scale")
-        for s in (k_scale, v_scale):
-            if s.dtype != torch.float32 or s.shape != (heads,) or not s.is_contiguous() or s.device != device:
-                raise ValueError("scales must be float32 [kv heads] on the cache's device")
-        dtype, ks, vs = _lib.CACHE_E4M3, k_scale.data_ptr(), v_scale.data_ptr()
-    elif k.dtype == torch.float16:
+    if dtype == _FP16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("scales belong to an e4m3 cache")
-        dtype, ks, vs = _lib.CACHE_F16, None, None
+        ks, vs, code = 0, 0, _lib.CACHE_F16
+    elif dtype == E4M3:
+        ks, vs, code = _scale(k_scale, heads), _scale(v_scale, heads), _lib.CACHE_E4M3
     else:
         raise ValueError("a cache is float16 or float8_e4m3fn")
-    return _lib.PagedCacheDesc(k.data_ptr(), v.data_ptr(), ks, vs, table.data_ptr(), pages, size,
-                               k.stride(0) if pages > 1 else heads * size * dh, heads, dh, table.shape[0],
-                               table.shape[1], table.stride(0) if table.shape[0] > 1 else table.shape[1], dtype)
-
-
-def _one_device(first, *ts):
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError("tensors must live on a CUDA device")
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors must live on one CUDA device")
-    return dev
+    return _pack(k.data_ptr(), v.data_ptr(), ks, vs, table.data_ptr(), pages, size,
+                 st[0] if pages > 1 else heads * size * dh, heads, dh, tsh[0], tsh[1],
+                 tst[0] if tsh[0] > 1 else tsh[1], code), heads, dh
 
 
 # ---------------------------------------------------------------- operators
@@ -104,11 +117,12 @@ def rope_table(Lmax: int, device, rot: int = 128, theta: float = ROPE_THETA, sca
         raise ValueError(f"scaling is None or one of {sorted(_lib.ROPE_KINDS)}")
     # `device` may be a bare "cuda": the tensor's own device has the index
     cs = torch.empty(Lmax, rot // 2, 2, dtype=torch.float32, device=device)
+    index = _device(cs)
     sc = None
     if scaling is not None:
         sc = ctypes.byref(_lib.RopeScaling(_lib.ROPE_KINDS[scaling], factor, context, low, high))
-    with _on(_one_device(cs)):
-        _lib.check(_lib.lib().tri_rope_table_scaled(_ptr(cs), Lmax, rot, float(theta), sc, _stream(cs.device)),
+    with _on(index):
+        _lib.check(_lib.lib().tri_rope_table_scaled(cs.data_ptr(), Lmax, rot, float(theta), sc, _raw_stream(index)),
                    "tri_rope_table_scaled")
     return cs
 
@@ -121,28 +135,27 @@ def qknorm_rope_append(qkv: torch.Tensor, pos: torch.Tensor, gq, gk, cs: torch.T
     (unless gq and gk are None) and rotated; keys (normed, rotated) and values
     written into the pages of their rows.  ``cs`` is a table of
     ``rope_table`` ([positions][rot/2][2]); the first rot features rotate."""
-    dev = _one_device(qkv, pos, gq, gk, cs, k, v, table, seq, out)
-    d = _desc(k, v, table, k_scale, v_scale, dev)
-    dh, T = d.head_dim, qkv.shape[0]
+    index = _device(qkv, pos, gq, gk, cs, k, v, table, seq, k_scale, v_scale, out)
+    cache, heads, dh = _cache(k, v, table, k_scale, v_scale)
     if qkv.dim() != 2:
         raise ValueError("qkv must be [rows][(H + 2 Hkv) * head dim]")
-    src, stride = _rows(qkv, (H + 2 * d.heads) * dh, "qkv")
-    if cs.dtype != torch.float32 or cs.dim() != 3 or cs.shape[2] != 2 or not cs.is_contiguous():
+    T = qkv.shape[0]
+    stride = _row_stride(qkv, T, (H + 2 * heads) * dh, "qkv")
+    if cs.dtype != _F32 or cs.dim() != 3 or cs.shape[2] != 2 or not cs.is_contiguous():
         raise ValueError("cs must be a contiguous float32 table [positions][rot / 2][2]")
     for g in (gq, gk):
-        if g is not None and (g.dtype != torch.float16 or g.shape != (dh,) or not g.is_contiguous()):
+        if g is not None and (g.dtype != _FP16 or g.shape != (dh,) or not g.is_contiguous()):
             raise ValueError("gains must be contiguous float16 [head dim]")
-    q = out if out is not None else torch.empty(T, H, dh, dtype=torch.float16, device=dev)
-    dst, q_stride = _rows(q, H * dh, "out")
-    if q.shape[0] != T:
-        raise ValueError("out must have one row per row of qkv")
+    q = out if out is not None else torch.empty(T, H, dh, dtype=_FP16, device=qkv.device)
+    q_stride = _row_stride(q, T, H * dh, "out")
+    pos_p, seq_p = _int32(pos, T, "pos"), None if seq is None else _int32(seq, T, "seq")
     if T == 0:
         return q
-    with _on(dev):
+    with _on(index):
         st = _lib.lib().tri_paged_qknorm_rope(
-            src, stride, _int32(pos, T, "pos"), None if seq is None else _int32(seq, T, "seq"), _ptr(gq) or None,
-            _ptr(gk) or None, cs.data_ptr(), cs.shape[0], 2 * cs.shape[1], int(bool(interleaved)), dst, q_stride,
-            ctypes.byref(d), T, H, eps, _stream(dev))
+            qkv.data_ptr(), stride, pos_p, seq_p, None if gq is None else gq.data_ptr(),
+            None if gk is None else gk.data_ptr(), cs.data_ptr(), cs.shape[0], 2 * cs.shape[1], 1 if interleaved else 0,
+            q.data_ptr(), q_stride, cache, T, H, eps, _raw_stream(index))
     if st:
         _lib.check(st, "tri_paged_qknorm_rope")
     return q
@@ -160,28 +173,26 @@ def attention_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: t
     ``scale`` defaults to 1 / sqrt(dh).  Without ``workspace`` each call takes
     its scratch from the caching allocator, so that calls on other streams and
     in captured graphs never share one."""
-    dev = _one_device(q, k, v, table, pos, seq, out)
-    d = _desc(k, v, table, k_scale, v_scale, dev)
-    if q.dim() != 3 or q.shape[2] != d.head_dim:
+    index = _device(q, k, v, table, pos, seq, k_scale, v_scale, out)
+    cache, heads, dh = _cache(k, v, table, k_scale, v_scale)
+    if q.dim() != 3 or q.shape[2] != dh:
         raise ValueError("q must be [rows][heads][head dim]")
-    M, H, dh = q.shape
-    src, stride = _rows(q, H * dh, "q")
-    y = out if out is not None else torch.empty(M, H * dh, dtype=torch.float16, device=dev)
-    dst, out_stride = _rows(y, H * dh, "out")
-    if y.shape[0] != M:
-        raise ValueError("out must have one row per row of q")
+    M, H, _ = q.shape
+    stride = _row_stride(q, M, H * dh, "q")
+    y = out if out is not None else torch.empty(M, H * dh, dtype=_FP16, device=q.device)
+    out_stride = _row_stride(y, M, H * dh, "out")
+    pos_p, seq_p = _int32(pos, M, "pos"), None if seq is None else _int32(seq, M, "seq")
     if M == 0:
         return y
     L = _lib.lib()
-    with _on(dev):
-        nbytes = max(int(L.tri_paged_attention_workspace_bytes(M, H, d.heads, dh)), 256)
-        ws = workspace.get(nbytes) if workspace is not None else torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if ws.device != dev:
+    with _on(index):
+        nbytes = L.tri_paged_attention_workspace_bytes(M, H, heads, dh) or 256
+        ws = workspace.get(nbytes) if workspace is not None else torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        if ws.get_device() != index:
             raise ValueError("the workspace must live on the tensors' device")
-        st = L.tri_paged_attention(src, stride, _int32(pos, M, "pos"), None if seq is None else _int32(seq, M, "seq"),
-                                   ctypes.byref(d), dst, out_stride, M, H,
-                                   1.0 / math.sqrt(dh) if scale is None else scale, ws.data_ptr(), ws.numel(),
-                                   _stream(dev))
+        st = L.tri_paged_attention(q.data_ptr(), stride, pos_p, seq_p, cache, y.data_ptr(), out_stride, M, H,
+                                   dh ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
+                                   _raw_stream(index))
     if st:
         _lib.check(st, "tri_paged_attention")
     return y
@@ -196,14 +207,15 @@ def copy_pages(pools: torch.Tensor, src, dst) -> None:
     in both), or int32 tensors on the device, which are not looked at on the
     host: pairs outside the pool are skipped, pages named twice end up with
     unspecified bytes."""
-    dev = _one_device(pools)
-    if pools.dim() < 4:
+    index = _device(pools)
+    shape, strides = pools.shape, pools.stride()
+    if len(shape) < 4:
         raise ValueError("pools must be [..., pages][kv heads][page size][head dim]")
-    lead, (pages, heads, size, dh) = pools.shape[:-4], pools.shape[-4:]
-    if pools.stride()[-3:] != (size * dh, dh, 1):
+    pages, heads, size, dh = shape[-4:]
+    if strides[-1] != 1 or strides[-2] != dh or (strides[-3] != size * dh and heads > 1):
         raise ValueError("the heads of a page must be contiguous")
     n_pools, pool_stride = 1, 0
-    for extent, stride in zip(reversed(lead), reversed(pools.stride()[:-4])):
+    for extent, stride in zip(reversed(shape[:-4]), reversed(strides[:-4])):
         if extent == 1:
             continue
         if n_pools == 1:
@@ -212,10 +224,9 @@ def copy_pages(pools: torch.Tensor, src, dst) -> None:
             raise ValueError("the pools must lie at one stride")
         n_pools *= extent
     if torch.is_tensor(src) and torch.is_tensor(dst):
+        _device(pools, src, dst)
         n = src.shape[0] if src.dim() else 0
-        if src.device != dev or dst.device != dev:
-            raise ValueError("tensors must live on one CUDA device")
-        pair = (_int32(src, n, "src"), _int32(dst, n, "dst"))
+        src_p, dst_p = _int32(src, n, "src"), _int32(dst, n, "dst")
     else:
         src, dst = [int(a) for a in src], [int(b) for b in dst]
         n = len(src)
@@ -225,15 +236,16 @@ def copy_pages(pools: torch.Tensor, src, dst) -> None:
             raise ValueError("page number out of range")
         if len(set(dst)) < n or set(src) & set(dst):
             raise ValueError("a page stands twice in dst, or in both src and dst")
-        both = torch.tensor([src, dst], dtype=torch.int32).to(dev)
-        pair = (both.data_ptr(), both.data_ptr() + 4 * n)
-    e = pools.element_size()
+        both = torch.tensor([src, dst], dtype=_I32).to(pools.device)
+        src_p, dst_p = both.data_ptr(), both.data_ptr() + 4 * n
     if n == 0 or n_pools == 0 or pages == 0:
         return
-    with _on(dev):
+    e = pools.element_size()
+    page_bytes = heads * size * dh * e
+    with _on(index):
         st = _lib.lib().tri_copy_pages(pools.data_ptr(), n_pools, pool_stride * e, pages,
-                                       (pools.stride(-4) if pages > 1 else heads * size * dh) * e,
-                                       heads * size * dh * e, pair[0], pair[1], n, _stream(dev))
+                                       strides[-4] * e if pages > 1 else page_bytes, page_bytes, src_p, dst_p, n,
+                                       _raw_stream(index))
     if st:
         _lib.check(st, "tri_copy_pages")
 
