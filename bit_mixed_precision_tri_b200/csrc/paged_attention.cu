@@ -374,6 +374,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       }
       c2 = p.scale * 1.4426950408889634f * (FP8 ? p.k_scale[d.head] : 1.f);
     }
+    if (d.pages != 0) {                                          // else nothing was loaded
     // ---- S^T = K Q^T
     float sc[NT][4], sc1[NT][4];                                 // two chains of dependent MMAs
 #pragma unroll
@@ -500,6 +501,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
       }
     }
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
     if (!(d.flags & kLast)) continue;
@@ -588,15 +590,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 }
 
 // Joins the partials of each split (row, head), in CTA order.  CTA (x, y): the
-// x-th record, float4s 32 y .. 32 y + 31 of the output; warp w sums every 8th
-// partial, then the eight sums are added in warp order.
+// x-th record, float4s 32 y .. 32 y + 31 of the output, which belong to eight
+// heads.  Warp w weighs the partials of one head and sums every 8th partial of the
+// outputs (the first 32 are on their way while the weights are formed: the chain of
+// dependent loads is what this kernel takes); the eight sums are added in warp
+// order.
 constexpr int kCombineThreads = 256;
 
 template <int DH, bool FP8, int NT>
 __global__ void __launch_bounds__(kCombineThreads)
 paged_combine_kernel(const Params p) {
-  extern __shared__ float wts[];                                 // [partials][8 NT]
-  __shared__ float inv[8 * NT];
+  extern __shared__ float wts[];                                 // [partials][8]
+  __shared__ float inv[8];
   __shared__ float4 sums[8][32];
   constexpr int kVec = DH / 16 * NT * 32;
   griddep_wait();                                                // in every CTA: the grid ends after its predecessor
@@ -605,44 +610,57 @@ paged_combine_kernel(const Params p) {
   if (J == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = rec.x / p.heads, head = rec.x % p.heads;
+  const int vec = blockIdx.y * 32 + lane, fb = blockIdx.y / NT, nt = blockIdx.y % NT;
   auto slot = [&](int j) -> int64_t { return 2 * (int64_t)(rec.y + j) + (j == 0 ? 1 : 0); };
-  for (int hd = warp; hd < 8 * NT; hd += 8) {
-    float top = -INFINITY;
-    for (int j = lane; j < J; j += 32) top = fmaxf(top, p.ml[slot(j) * 8 * NT + hd].x);
+  float4 v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (warp + 8 * k < J) v[k] = p.part[slot(warp + 8 * k) * kVec + vec];
+  {
+    const float2* ml = p.ml + 8 * nt + warp;
+    const float2 none = make_float2(-INFINITY, 0.f), first = lane < J ? ml[slot(lane) * 8 * NT] : none;
+    float top = first.x;
+    for (int j = lane + 32; j < J; j += 32) top = fmaxf(top, ml[slot(j) * 8 * NT].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
     for (int j = lane; j < J; j += 32) {
-      const float2 v = p.ml[slot(j) * 8 * NT + hd];
-      const float w = ex2(v.x - base);
-      wts[j * 8 * NT + hd] = w;
-      sum = fmaf(w, v.y, sum);
+      const float2 u = j == lane ? first : ml[slot(j) * 8 * NT];
+      const float w = ex2(u.x - base);
+      wts[j * 8 + warp] = w;
+      sum = fmaf(w, u.y, sum);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) inv[hd] = sum == 0.f ? 0.f : (FP8 ? p.v_scale[head] : 1.f) / sum;
+    if (lane == 0) inv[warp] = sum == 0.f ? 0.f : (FP8 ? p.v_scale[head] : 1.f) / sum;
   }
   __syncthreads();
-  const int vec = blockIdx.y * 32 + lane, block = vec >> 5, fb = block / NT, nt = block % NT;
-  const int gid = lane >> 2, tig = lane & 3, h0 = 8 * nt + 2 * tig;
+  const int gid = lane >> 2, tig = lane & 3;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = warp; j < J; j += 8) {
-    const float4 v = p.part[slot(j) * kVec + vec];
-    const float a = wts[j * 8 * NT + h0], b = wts[j * 8 * NT + h0 + 1];
-    acc.x = fmaf(a, v.x, acc.x), acc.y = fmaf(b, v.y, acc.y);
-    acc.z = fmaf(a, v.z, acc.z), acc.w = fmaf(b, v.w, acc.w);
+  for (int j0 = warp; j0 < J; j0 += 32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + 8 * k;
+      if (j >= J) break;
+      const float2 w = *reinterpret_cast<const float2*>(&wts[j * 8 + 2 * tig]);
+      acc.x = fmaf(w.x, v[k].x, acc.x), acc.y = fmaf(w.y, v[k].y, acc.y);
+      acc.z = fmaf(w.x, v[k].z, acc.z), acc.w = fmaf(w.y, v[k].w, acc.w);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (j0 + 32 + 8 * k < J) v[k] = p.part[slot(j0 + 32 + 8 * k) * kVec + vec];
   }
   sums[warp][lane] = acc;
   __syncthreads();
   if (warp != 0) return;
 #pragma unroll
   for (int w = 1; w < 8; ++w) {
-    const float4 v = sums[w][lane];
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    const float4 u = sums[w][lane];
+    acc.x += u.x, acc.y += u.y, acc.z += u.z, acc.w += u.w;
   }
-  __half* dst = p.out + (int64_t)row * p.out_stride + (int64_t)head * p.G * DH;
-  store_out<DH, FP8>(dst, h0, p.G, 16 * fb, gid, acc, inv[h0], inv[h0 + 1]);
+  store_out<DH, FP8>(p.out + (int64_t)row * p.out_stride + (int64_t)head * p.G * DH, 8 * nt + 2 * tig, p.G, 16 * fb,
+                     gid, acc, inv[2 * tig], inv[2 * tig + 1]);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn_p() {
@@ -721,7 +739,7 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
   const int64_t segs = p.M * p.heads;
   cfg.gridDim = dim3((unsigned)(segs < ctas ? segs : ctas), DH / 16 * NT);
   cfg.blockDim = dim3(kCombineThreads);
-  cfg.dynamicSmemBytes = (size_t)ctas * 8 * NT * sizeof(float);
+  cfg.dynamicSmemBytes = (size_t)ctas * 8 * sizeof(float);
   return cudaLaunchKernelEx(&cfg, paged_combine_kernel<DH, FP8, NT>, p);
 }
 
