@@ -5,7 +5,7 @@
 // What bounds it: every key and value is read once for the G = H / heads query
 // heads that share it, 4 G flops per element: HBM bandwidth.
 //
-//  * Work = tiles of 64 positions of one (row, key/value head), in the order
+//  * Work = tiles of 64 or 128 positions of one (row, key/value head), in the order
 //    row, head, tile; every CTA takes an equal run of them, so ragged lengths
 //    load the SMs alike and the host needs no length.  A run covers the end of
 //    one (row, head), whole ones, and the start of another: whole ones are
@@ -16,7 +16,7 @@
 //    bytes of each, hardware-swizzled), and the row's queries with the first
 //    tile.  Absent pages are not loaded.  A descriptor per stage says what the
 //    tile is.
-//  * Four consumer warps take 16 positions of a tile each.  Scores are formed
+//  * Four consumer warps take 16 or 32 positions of a tile each.  Scores are formed
 //    transposed, S^T = K Q^T (mma.sync m16n8k16: positions are the 16 rows, up
 //    to 8 query heads the columns, so that no row is wasted on heads that do not
 //    exist), with the running maximum and sum in fp32 per warp.  O^T += V^T P^T:
@@ -36,8 +36,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTile = 64;                    // positions per stage
-constexpr int kWarps = 4;                    // consumer warps, 16 positions each
+constexpr int kWarps = 4;                    // consumer warps, 16 or 32 positions of a tile each
 constexpr int kThreads = 32 * (kWarps + 1);  // and the producer warp
 constexpr int kMaxStages = 8;
 constexpr uint32_t kWaitPolls = 1u << 18;    // about a second
@@ -46,6 +45,13 @@ constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
 template <int DH, bool FP8, int NT>
 struct Cfg {
   static constexpr int kRow = DH * (FP8 ? 1 : 2);             // bytes of a position
+  // A warp's chain of dependent steps per tile (scores, maximum, weights, output)
+  // takes about 0.7 us whatever its width, so rows of at most 128 bytes come 128 to
+  // a tile (two sets of 16 per warp); 256-byte ones, for which HBM is slower than
+  // that chain, 64, and more than 8 query heads, two chains by themselves, too.
+  static constexpr int kSets = kRow <= 128 && NT == 1 ? 2 : 1;
+  static constexpr int kTile = 64 * kSets;                    // positions per stage
+  static constexpr int kTileShift = kSets == 2 ? 7 : 6;
   static constexpr int kBox = kRow < 128 ? kRow : 128;        // bytes of it in one box
   static constexpr int kParts = kRow / kBox;
   static constexpr int kKV = kTile * kRow;                    // bytes of a K (or V) tile
@@ -127,7 +133,6 @@ __device__ __forceinline__ int row_length(const Params& p, int64_t m, int& s) {
   if (s < 0 || s >= p.seqs || L < 0) return 0;
   return L < p.max_len ? L + 1 : p.max_len;
 }
-__device__ __forceinline__ int row_tiles(int L) { return (L + kTile - 1) / kTile; }
 
 // the runs: the first `rem` CTAs take base + 1 tiles
 struct Runs {
@@ -167,7 +172,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   __shared__ float2 wml[kWarps][8 * NT];
   __shared__ long long sums[kWarps + 1], s_first_prefix;
   __shared__ int s_first_row;
+  constexpr int kTile = C::kTile, kTileShift = C::kTileShift, kSets = C::kSets;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto row_tiles = [](int len) { return (len + kTile - 1) >> kTileShift; };
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -238,7 +245,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
     const uint64_t policy = policy_evict_first();
-    const int shift = p.page_shift, rows = shift < 6 ? 1 << shift : kTile;   // of a box
+    const int shift = p.page_shift, rows = shift < kTileShift ? 1 << shift : kTile;   // of a box
     const int npg = kTile / rows, nbox = npg * C::kParts * 2;
     const int pi = lane % npg, part = (lane / npg) % C::kParts, kv = lane / (npg * C::kParts);
     const uint32_t box_dst = (uint32_t)(kv * C::kKV + part * kTile * C::kBox + pi * rows * C::kBox);
@@ -311,7 +318,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         bulk_load(qring + st * C::kQ + lane * C::kQRow, p.q + (int64_t)cm * p.q_stride + ((int64_t)ch * p.G + lane) * DH,
                   DH * 2, &full[st]);
       if (cid >= 0) {
-        const int in_page = shift > 6 ? (int)(((int64_t)ct * kTile) & ((1 << shift) - 1)) : 0;
+        const int in_page = shift > kTileShift ? (int)(((int64_t)ct * kTile) & ((1 << shift) - 1)) : 0;
         tma_load_3d(smem_u32(sm) + (uint32_t)(st * 2 * C::kKV) + box_dst, kv ? &vmap : &kmap, box_x,
                     (ch << shift) + in_page, cid, &full[st], policy);
       }
@@ -326,12 +333,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
   // -------------------------------------------------------------- consumers
   const int gid = lane >> 2, tig = lane & 3;
-  const int page_shift = p.page_shift < 6 ? p.page_shift : 6;
+  const int page_shift = p.page_shift < kTileShift ? p.page_shift : kTileShift;
   // ldmatrix rows and 16-byte chunks: K (and e4m3 V): rows (lane & 7) + 8 (lane
   // >> 3 & 1), chunk + (lane >> 4); fp16 V transposed: rows (lane & 7) + 8 (lane
   // >> 4), chunk + (lane >> 3 & 1)
-  const int r_a = 16 * warp + (lane & 7) + 8 * ((lane >> 3) & 1), c_a = lane >> 4;
-  const int r_t = 16 * warp + (lane & 7) + 8 * (lane >> 4), c_t = (lane >> 3) & 1;
+  const int r_a = 16 * kSets * warp + (lane & 7) + 8 * ((lane >> 3) & 1), c_a = lane >> 4;
+  const int r_t = 16 * kSets * warp + (lane & 7) + 8 * (lane >> 4), c_t = (lane >> 3) & 1;
   auto address = [&](uint32_t base, int row, int chunk) -> uint32_t {
     if constexpr (C::kBox == 128)
       return base + (uint32_t)((chunk >> 3) * kTile * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
@@ -376,69 +383,97 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     if (d.pages != 0) {                                          // else nothing was loaded
     // ---- S^T = K Q^T
-    float sc[NT][4], sc1[NT][4];                                 // two chains of dependent MMAs
+    float sc[kSets][NT][4];
+    if constexpr (kSets == 1 && !FP8) {                          // two chains of dependent MMAs
+      float odd[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] = sc1[nt][e] = 0.f;
-    if constexpr (FP8) {
-#pragma unroll
-      for (int kp = 0; kp < DH / 32; ++kp) {
-        uint32_t r[4];
-        ldsm_x4(address(kbase, r_a, 2 * kp + c_a), r);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t a[4];
-          e4m3x4_to_half2(r[2 * k], a[0], a[2]);
-          e4m3x4_to_half2(r[2 * k + 1], a[1], a[3]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(k ? sc1[nt] : sc[nt], a, qf[2 * kp + k][nt][0], qf[2 * kp + k][nt][1]);
-        }
-      }
-    } else {
+        for (int e = 0; e < 4; ++e) sc[0][nt][e] = odd[nt][e] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < DH / 16; ++kk) {
         uint32_t a[4];
         ldsm_x4(address(kbase, r_a, 2 * kk + c_a), a);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816(kk & 1 ? sc1[nt] : sc[nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_16816(kk & 1 ? odd[nt] : sc[0][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[0][nt][e] += odd[nt][e];
+    } else {
+#pragma unroll
+      for (int u = 0; u < kSets; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[u][nt][e] = 0.f;
+      if constexpr (FP8) {
+#pragma unroll
+        for (int kp = 0; kp < DH / 32; ++kp)
+#pragma unroll
+          for (int u = 0; u < kSets; ++u) {
+            uint32_t r[4];
+            ldsm_x4(address(kbase, r_a + 16 * u, 2 * kp + c_a), r);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t a[4];
+              e4m3x4_to_half2(r[2 * k], a[0], a[2]);
+              e4m3x4_to_half2(r[2 * k + 1], a[1], a[3]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816(sc[u][nt], a, qf[2 * kp + k][nt][0], qf[2 * kp + k][nt][1]);
+            }
+          }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+          for (int u = 0; u < kSets; ++u) {
+            uint32_t a[4];
+            ldsm_x4(address(kbase, r_a + 16 * u, 2 * kk + c_a), a);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(sc[u][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+          }
       }
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] += sc1[nt][e];
     // ---- positions that do not count (behind the row's end, in absent pages): no
     // weight, and a weight of zero times a NaN would be NaN, so their V rows are
     // cleared in the stage before they are read
     if (d.nval != kTile || d.pages != (1 << (kTile >> page_shift)) - 1) {
       auto valid = [&](int r) { return r < d.nval && ((d.pages >> (r >> page_shift)) & 1); };
-      const bool v0 = valid(16 * warp + gid), v1 = valid(16 * warp + gid + 8);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (!v0) sc[nt][0] = sc[nt][1] = -INFINITY;
-        if (!v1) sc[nt][2] = sc[nt][3] = -INFINITY;
-      }
-      const int r = 16 * warp + (lane >> 1);                     // two lanes a row
-      if (!valid(r))
+      for (int u = 0; u < kSets; ++u) {
+        const int set = 16 * (kSets * warp + u);
+        const bool v0 = valid(set + gid), v1 = valid(set + gid + 8);
 #pragma unroll
-        for (int c = 0; c < C::kRow / 32; ++c) {
-          const uint32_t a = address(vbase, r, 2 * c + (lane & 1));
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+        for (int nt = 0; nt < NT; ++nt) {
+          if (!v0) sc[u][nt][0] = sc[u][nt][1] = -INFINITY;
+          if (!v1) sc[u][nt][2] = sc[u][nt][3] = -INFINITY;
         }
+        const int r = set + (lane >> 1);                         // two lanes a row
+        if (!valid(r))
+#pragma unroll
+          for (int c = 0; c < C::kRow / 32; ++c) {
+            const uint32_t a = address(vbase, r, 2 * c + (lane & 1));
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+          }
+      }
       fence_proxy_async();                                       // before TMA refills the stage
       __syncwarp();
     }
-    // ---- running softmax; the eight lanes of a column hold its 16 positions
-    uint32_t ph[NT][2], pl[NT][2];
+    // ---- running softmax; the eight lanes of a column hold the positions of a set
+    uint32_t ph[kSets][NT][2], pl[kSets][NT][2];
     bool grew = false;
     float alpha[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float pr[4];
+      float pr[kSets][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float top = fmaxf(sc[nt][e], sc[nt][2 + e]) * c2;
+        float top = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
+#pragma unroll
+        for (int u = 1; u < kSets; ++u) top = fmaxf(top, fmaxf(sc[u][nt][e], sc[u][nt][2 + e]));
+        top *= c2;
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
@@ -447,19 +482,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         alpha[nt][e] = ex2(mx[nt][e] - base);
         grew |= mnew > mx[nt][e];
         mx[nt][e] = mnew;
-        pr[e] = ex2(fmaf(sc[nt][e], c2, -base));
-        pr[2 + e] = ex2(fmaf(sc[nt][2 + e], c2, -base));
-      }
-      ph[nt][0] = half2_bits(pr[0], pr[1]);
-      ph[nt][1] = half2_bits(pr[2], pr[3]);
-      const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&ph[nt][0]));
-      const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&ph[nt][1]));
-      pl[nt][0] = transpose8x8(half2_bits(pr[0] - h0.x, pr[1] - h0.y));
-      pl[nt][1] = transpose8x8(half2_bits(pr[2] - h1.x, pr[3] - h1.y));
-      ph[nt][0] = transpose8x8(ph[nt][0]);
-      ph[nt][1] = transpose8x8(ph[nt][1]);
+        float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) l[nt][e] = fmaf(l[nt][e], alpha[nt][e], pr[e] + pr[2 + e]);
+        for (int u = 0; u < kSets; ++u) {
+          pr[u][e] = ex2(fmaf(sc[u][nt][e], c2, -base));
+          pr[u][2 + e] = ex2(fmaf(sc[u][nt][2 + e], c2, -base));
+          sum += pr[u][e] + pr[u][2 + e];
+        }
+        l[nt][e] = fmaf(l[nt][e], alpha[nt][e], sum);
+      }
+#pragma unroll
+      for (int u = 0; u < kSets; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t hi = half2_bits(pr[u][2 * r], pr[u][2 * r + 1]);
+          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          pl[u][nt][r] = transpose8x8(half2_bits(pr[u][2 * r] - h.x, pr[u][2 * r + 1] - h.y));
+          ph[u][nt][r] = transpose8x8(hi);
+        }
     }
     if (__any_sync(0xFFFFFFFFu, grew)) {                         // rare after the first tiles
 #pragma unroll
@@ -473,33 +513,37 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // ---- O^T += V^T P^T
     if constexpr (FP8) {
 #pragma unroll
-      for (int fp = 0; fp < DH / 32; ++fp) {
-        uint32_t r[4];
-        ldsm_x4_t(address(vbase, r_a, 2 * fp + c_a), r);
+      for (int fp = 0; fp < DH / 32; ++fp)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          // bytes: position 2 tig, features 2 gid and 2 gid + 1; position 2 tig + 1, the same
-          uint32_t a[4];
-          e4m3x4_to_half2(__byte_perm(r[2 * k], 0, 0x3120), a[0], a[1]);
-          e4m3x4_to_half2(__byte_perm(r[2 * k + 1], 0, 0x3120), a[2], a[3]);
+        for (int u = 0; u < kSets; ++u) {
+          uint32_t r[4];
+          ldsm_x4_t(address(vbase, r_a + 16 * u, 2 * fp + c_a), r);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_16816(o[2 * fp + k][nt], a, ph[nt][0], ph[nt][1]);
-            mma_16816(o[2 * fp + k][nt], a, pl[nt][0], pl[nt][1]);
+          for (int k = 0; k < 2; ++k) {
+            // bytes: position 2 tig, features 2 gid and 2 gid + 1; position 2 tig + 1, the same
+            uint32_t a[4];
+            e4m3x4_to_half2(__byte_perm(r[2 * k], 0, 0x3120), a[0], a[1]);
+            e4m3x4_to_half2(__byte_perm(r[2 * k + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16816(o[2 * fp + k][nt], a, ph[u][nt][0], ph[u][nt][1]);
+              mma_16816(o[2 * fp + k][nt], a, pl[u][nt][0], pl[u][nt][1]);
+            }
           }
         }
-      }
     } else {
 #pragma unroll
-      for (int fb = 0; fb < DH / 16; ++fb) {
-        uint32_t a[4];
-        ldsm_x4_t(address(vbase, r_t, 2 * fb + c_t), a);
+      for (int fb = 0; fb < DH / 16; ++fb)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_16816(o[fb][nt], a, ph[nt][0], ph[nt][1]);
-          mma_16816(o[fb][nt], a, pl[nt][0], pl[nt][1]);
+        for (int u = 0; u < kSets; ++u) {
+          uint32_t a[4];
+          ldsm_x4_t(address(vbase, r_t + 16 * u, 2 * fb + c_t), a);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(o[fb][nt], a, ph[u][nt][0], ph[u][nt][1]);
+            mma_16816(o[fb][nt], a, pl[u][nt][0], pl[u][nt][1]);
+          }
         }
-      }
     }
     }
     __syncwarp();
@@ -700,7 +744,7 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
     const cuuint64_t dims[3] = {(cuuint64_t)DH, (cuuint64_t)(c.heads * c.page_size), (cuuint64_t)c.pages};
     const cuuint64_t strides[2] = {(cuuint64_t)K::kRow, (cuuint64_t)c.page_stride * (FP8 ? 1 : 2)};
     const cuuint32_t box[3] = {(cuuint32_t)(K::kBox / (FP8 ? 1 : 2)),
-                               (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile), 1};
+                               (cuuint32_t)(c.page_size < K::kTile ? c.page_size : K::kTile), 1};
     const cuuint32_t es[3] = {1, 1, 1};
     if (enc(&maps[i], FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, i ? c.v : c.k, dims,
             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -719,7 +763,7 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
     if (dev < 64) ready[dev] = true;
   }
   // no more CTAs than tiles can exist
-  const int64_t most = p.M * p.heads * (int64_t)((p.max_len + kTile - 1) / kTile);
+  const int64_t most = p.M * p.heads * (int64_t)((p.max_len + K::kTile - 1) / K::kTile);
   const int64_t ctas = most < (int64_t)K::kCtasPerSm * sms ? most : (int64_t)K::kCtasPerSm * sms;
   const Space w = space(ctas, NT, DH);
   p.recs = static_cast<int4*>(ws);
