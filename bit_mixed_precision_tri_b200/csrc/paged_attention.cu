@@ -11,9 +11,9 @@
 //    one (row, head), whole ones, and the start of another: whole ones are
 //    written at once, the two open ends leave a (max, sum, output) partial in
 //    the workspace, and paged_combine_kernel joins each split (row, head).
-//  * One producer warp walks the run, looks the pages up one tile ahead and
-//    loads K and V with TMA into a ring of stages (a box is one page's rows, 128
-//    bytes of each, hardware-swizzled), and the row's queries with the first
+//  * Two producer warps, of K and of V, walk the run, look the pages up one tile
+//    ahead and load them with TMA into a ring of stages (a box is one page's rows,
+//    128 bytes of each, hardware-swizzled), and the row's queries with the first
 //    tile.  Absent pages are not loaded.  A descriptor per stage says what the
 //    tile is.
 //  * Four consumer warps take 16 or 32 positions of a tile each.  Scores are formed
@@ -37,8 +37,9 @@ namespace {
 using namespace ptx;
 
 constexpr int kWarps = 4;                    // consumer warps, 16 or 32 positions of a tile each
-constexpr int kThreads = 32 * (kWarps + 1);  // and the producer warp
+constexpr int kThreads = 32 * (kWarps + 2);  // and two producer warps, of K and of V
 constexpr int kMaxStages = 8;
+constexpr int kSoloRun = 2;                  // a run of more tiles gives one-tile (row, head)s to single warps
 constexpr uint32_t kWaitPolls = 1u << 18;    // about a second
 constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
 
@@ -74,7 +75,7 @@ struct Desc {                 // what a stage holds
   int pages;                  // bit i: the tile's i-th page was loaded
   int flags;
 };
-constexpr int kFirst = 1, kLast = 2, kOpenLeft = 4, kOpenRight = 8;
+constexpr int kFirst = 1, kLast = 2, kOpenLeft = 4, kOpenRight = 8, kSolo = 16;
 
 struct Params {
   const __half* q;
@@ -145,6 +146,15 @@ struct Runs {
   }
 };
 
+// a row's 16-byte chunk in a K or V tile, as the TMA swizzle places it
+template <typename C>
+__device__ __forceinline__ uint32_t tile_address(uint32_t base, int row, int chunk) {
+  if constexpr (C::kBox == 128)
+    return base + (uint32_t)((chunk >> 3) * C::kTile * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+  else
+    return base + (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+
 // a lane's four sums of a feature block: heads h0 and h0 + 1 of (x, z) and (y, w)
 template <int DH, bool FP8>
 __device__ __forceinline__ void store_out(__half* dst, int h0, int G, int f, int gid, float4 y, float i0, float i1) {
@@ -170,7 +180,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   __shared__ uint64_t full[C::kStages], empty[C::kStages];
   __shared__ Desc desc[C::kStages];
   __shared__ float2 wml[kWarps][8 * NT];
-  __shared__ long long sums[kWarps + 1], s_first_prefix;
+  __shared__ long long sums[kWarps + 2], s_first_prefix;
   __shared__ int s_first_row;
   constexpr int kTile = C::kTile, kTileShift = C::kTileShift, kSets = C::kSets;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -178,15 +188,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);
       mbar_init(&empty[s], kWarps);
     }
     fence_mbar_init();
   }
-  if (warp == kWarps && lane == 0) {
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
-  }
+  if (warp >= kWarps && lane == 0) prefetch_tensormap(warp == kWarps ? &kmap : &vmap);
   griddep_launch_dependents();
   griddep_wait();
 
@@ -208,7 +215,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w <= kWarps; ++w) {
+  for (int w = 0; w < kWarps + 2; ++w) {
     if (w < warp) before += sums[w];
     total += sums[w];
   }
@@ -242,13 +249,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     return;
   }
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer
+  if (warp >= kWarps) {
+    // ------------------------------------------------------------ producers
+    const bool is_v = warp > kWarps;
     const uint64_t policy = policy_evict_first();
     const int shift = p.page_shift, rows = shift < kTileShift ? 1 << shift : kTile;   // of a box
-    const int npg = kTile / rows, nbox = npg * C::kParts * 2;
-    const int pi = lane % npg, part = (lane / npg) % C::kParts, kv = lane / (npg * C::kParts);
-    const uint32_t box_dst = (uint32_t)(kv * C::kKV + part * kTile * C::kBox + pi * rows * C::kBox);
+    const int npg = kTile / rows, nbox = npg * C::kParts;
+    const int pi = lane % npg, part = lane / npg;
+    const uint32_t box_dst = (uint32_t)((is_v ? C::kKV : 0) + part * kTile * C::kBox + pi * rows * C::kBox);
     const int box_x = part * (C::kBox / (FP8 ? 1 : 2));
     int64_t m = s_first_row;
     int s, L = row_length(p, m, s), T = row_tiles(L);
@@ -289,7 +297,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       }
       const bool first = i == 0 || ct == 0, last = i + 1 == ntiles || ct == cT - 1;
       const unsigned loaded = __ballot_sync(0xFFFFFFFFu, cid >= 0);
-      if (lane == 0) {
+      if (lane == 0 && !is_v) {
         Desc d;
         d.row = cm, d.head = ch;
         const int64_t left = (int64_t)cL - (int64_t)ct * kTile;
@@ -301,6 +309,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           const bool open_r = ct != cT - 1;
           d.flags |= (open_l ? kOpenLeft : 0) | (open_r ? kOpenRight : 0);
         }
+        if (ct == 0 && cT == 1 && ntiles > kSoloRun) d.flags |= kSolo;
         desc[st] = d;
         // the CTA that holds the first tile of a (row, head) says who joins it
         if (ct == 0) {
@@ -311,19 +320,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           if (by_seg) p.recs[seg] = rec;
           else if (split) split_rec = rec;
         }
-        mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(loaded) * rows * C::kBox + (first ? p.G * DH * 2 : 0)));
       }
+      if (lane == 0)
+        mbar_arrive_expect_tx(&full[st],
+                              (uint32_t)(__popc(loaded) * rows * C::kBox + (first && !is_v ? p.G * DH * 2 : 0)));
       __syncwarp();
-      if (first && lane < p.G)
+      if (first && !is_v && lane < p.G)
         bulk_load(qring + st * C::kQ + lane * C::kQRow, p.q + (int64_t)cm * p.q_stride + ((int64_t)ch * p.G + lane) * DH,
                   DH * 2, &full[st]);
       if (cid >= 0) {
         const int in_page = shift > kTileShift ? (int)(((int64_t)ct * kTile) & ((1 << shift) - 1)) : 0;
-        tma_load_3d(smem_u32(sm) + (uint32_t)(st * 2 * C::kKV) + box_dst, kv ? &vmap : &kmap, box_x,
+        tma_load_3d(smem_u32(sm) + (uint32_t)(st * 2 * C::kKV) + box_dst, is_v ? &vmap : &kmap, box_x,
                     (ch << shift) + in_page, cid, &full[st], policy);
       }
     }
-    if (lane == 0 && !by_seg) p.recs[blockIdx.x] = split_rec;
+    if (lane == 0 && !is_v && !by_seg) p.recs[blockIdx.x] = split_rec;
     // every copy has landed before the CTA may leave
     for (int64_t i = ntiles > C::kStages ? ntiles - C::kStages : 0; i < ntiles; ++i)
       if (!mbar_wait(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1, kWaitPolls) && lane == 0)
@@ -337,14 +348,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   // ldmatrix rows and 16-byte chunks: K (and e4m3 V): rows (lane & 7) + 8 (lane
   // >> 3 & 1), chunk + (lane >> 4); fp16 V transposed: rows (lane & 7) + 8 (lane
   // >> 4), chunk + (lane >> 3 & 1)
-  const int r_a = 16 * kSets * warp + (lane & 7) + 8 * ((lane >> 3) & 1), c_a = lane >> 4;
-  const int r_t = 16 * kSets * warp + (lane & 7) + 8 * (lane >> 4), c_t = (lane >> 3) & 1;
-  auto address = [&](uint32_t base, int row, int chunk) -> uint32_t {
-    if constexpr (C::kBox == 128)
-      return base + (uint32_t)((chunk >> 3) * kTile * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-    else
-      return base + (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
-  };
+  const int r_a = (lane & 7) + 8 * ((lane >> 3) & 1), c_a = lane >> 4;
+  const int r_t = (lane & 7) + 8 * (lane >> 4), c_t = (lane >> 3) & 1;
+  auto address = [](uint32_t base, int row, int chunk) { return tile_address<C>(base, row, chunk); };
   uint32_t qf[DH / 16][NT][2];
   float o[DH / 16][NT][4];
   float mx[NT][2], l[NT][2];
@@ -359,6 +365,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     __syncwarp();
     const Desc d = desc[st];
+    // a one-tile (row, head) in a longer run is one warp's, with no merge; its
+    // neighbours are the other warps'
+    const bool solo = d.flags & kSolo;
+    if (solo && (int)(i & (kWarps - 1)) != warp) {
+      if (lane == 0) mbar_arrive(&empty[st]);
+      continue;
+    }
     const uint32_t kbase = smem_u32(sm) + (uint32_t)(st * 2 * C::kKV), vbase = kbase + C::kKV;
     if (d.flags & kFirst) {
       const uint32_t qb = smem_u32(qring + st * C::kQ);
@@ -381,7 +394,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       }
       c2 = p.scale * 1.4426950408889634f * (FP8 ? p.k_scale[d.head] : 1.f);
     }
-    if (d.pages != 0) {                                          // else nothing was loaded
+    // blocks of 16 kSets positions: this warp's, or all; none past the row's end,
+    // none where nothing was loaded
+    const int blocks = d.pages == 0 ? 0 : (d.nval + 16 * kSets - 1) / (16 * kSets);
+    const int blk_end = solo ? blocks : (warp < blocks ? warp + 1 : 0);
+    for (int blk = solo ? 0 : warp; blk < blk_end; ++blk) {
+    const int r0 = 16 * kSets * blk;
     // ---- S^T = K Q^T
     float sc[kSets][NT][4];
     if constexpr (kSets == 1 && !FP8) {                          // two chains of dependent MMAs
@@ -393,7 +411,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
       for (int kk = 0; kk < DH / 16; ++kk) {
         uint32_t a[4];
-        ldsm_x4(address(kbase, r_a, 2 * kk + c_a), a);
+        ldsm_x4(address(kbase, r0 + r_a, 2 * kk + c_a), a);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_16816(kk & 1 ? odd[nt] : sc[0][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
       }
@@ -414,7 +432,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
           for (int u = 0; u < kSets; ++u) {
             uint32_t r[4];
-            ldsm_x4(address(kbase, r_a + 16 * u, 2 * kp + c_a), r);
+            ldsm_x4(address(kbase, r0 + r_a + 16 * u, 2 * kp + c_a), r);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               uint32_t a[4];
@@ -430,7 +448,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
           for (int u = 0; u < kSets; ++u) {
             uint32_t a[4];
-            ldsm_x4(address(kbase, r_a + 16 * u, 2 * kk + c_a), a);
+            ldsm_x4(address(kbase, r0 + r_a + 16 * u, 2 * kk + c_a), a);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_16816(sc[u][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
           }
@@ -443,7 +461,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       auto valid = [&](int r) { return r < d.nval && ((d.pages >> (r >> page_shift)) & 1); };
 #pragma unroll
       for (int u = 0; u < kSets; ++u) {
-        const int set = 16 * (kSets * warp + u);
+        const int set = r0 + 16 * u;
         const bool v0 = valid(set + gid), v1 = valid(set + gid + 8);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -517,7 +535,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
         for (int u = 0; u < kSets; ++u) {
           uint32_t r[4];
-          ldsm_x4_t(address(vbase, r_a + 16 * u, 2 * fp + c_a), r);
+          ldsm_x4_t(address(vbase, r0 + r_a + 16 * u, 2 * fp + c_a), r);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             // bytes: position 2 tig, features 2 gid and 2 gid + 1; position 2 tig + 1, the same
@@ -537,7 +555,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
         for (int u = 0; u < kSets; ++u) {
           uint32_t a[4];
-          ldsm_x4_t(address(vbase, r_t + 16 * u, 2 * fb + c_t), a);
+          ldsm_x4_t(address(vbase, r0 + r_t + 16 * u, 2 * fb + c_t), a);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_16816(o[fb][nt], a, ph[u][nt][0], ph[u][nt][1]);
@@ -550,6 +568,27 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     if (lane == 0) mbar_arrive(&empty[st]);
     if (!(d.flags & kLast)) continue;
 
+    const float vs = FP8 ? p.v_scale[d.head] : 1.f;
+    __half* dst = p.out + (int64_t)d.row * p.out_stride + (int64_t)d.head * p.G * DH;
+    if (solo) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float i2[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = l[nt][e];
+          v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+          v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+          v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+          i2[e] = v == 0.f ? 0.f : vs / v;
+        }
+#pragma unroll
+        for (int fb = 0; fb < DH / 16; ++fb)
+          store_out<DH, FP8>(dst, 8 * nt + 2 * tig, p.G, 16 * fb, gid,
+                             make_float4(o[fb][nt][0], o[fb][nt][1], o[fb][nt][2], o[fb][nt][3]), i2[0], i2[1]);
+      }
+      continue;
+    }
     // ---- the four warps' (max, sum, output) into one, in warp order
     float f[NT][2], lsum[NT][2], mtop[NT][2];
 #pragma unroll
@@ -610,8 +649,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // every warp adds and stores a quarter of the features
     const bool open = d.flags & (kOpenLeft | kOpenRight);
     const int64_t slot = 2 * (int64_t)blockIdx.x + ((d.flags & kOpenLeft) ? 0 : 1);
-    const float vs = FP8 ? p.v_scale[d.head] : 1.f;
-    __half* dst = p.out + (int64_t)d.row * p.out_stride + (int64_t)d.head * p.G * DH;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int h0 = 8 * nt + 2 * tig;
