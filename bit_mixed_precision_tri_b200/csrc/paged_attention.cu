@@ -88,7 +88,7 @@ struct Params {
   float4* part;               // [2 CTAs][DH/16][NT][32 lanes]
   unsigned* error;
   int64_t q_stride, out_stride, table_stride, M;
-  int heads, G, page_shift, pages, seqs, max_len;
+  int heads, G, page_shift, pages, seqs, max_len, ctas;
   float scale;
 };
 
@@ -688,7 +688,8 @@ paged_combine_kernel(const Params p) {
   griddep_wait();                                                // in every CTA: the grid ends after its predecessor
   const int4 rec = p.recs[blockIdx.x];
   const int J = rec.z;
-  if (J == 0) return;
+  // 0: not split.  A record that no call wrote (a workspace that unordered calls share) is not followed.
+  if (J <= 0 || rec.y < 0 || J > p.ctas - rec.y || rec.x < 0 || rec.x >= p.M * p.heads) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = rec.x / p.heads, head = rec.x % p.heads;
   const int vec = blockIdx.y * 32 + lane, fb = blockIdx.y / NT, nt = blockIdx.y % NT;
@@ -802,6 +803,7 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
   // no more CTAs than tiles can exist
   const int64_t most = p.M * p.heads * (int64_t)((p.max_len + K::kTile - 1) / K::kTile);
   const int64_t ctas = most < (int64_t)K::kCtasPerSm * sms ? most : (int64_t)K::kCtasPerSm * sms;
+  p.ctas = (int)ctas;
   const Space w = space(ctas, NT, DH);
   p.recs = static_cast<int4*>(ws);
   p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + w.ml);
@@ -817,6 +819,7 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<DH, FP8, NT>, maps[0], maps[1], p)) != cudaSuccess) return e;
+  if (p.max_len <= K::kTile) return cudaSuccess;                 // one tile a row at most: nothing is split
   const int64_t segs = p.M * p.heads;
   cfg.gridDim = dim3((unsigned)(segs < ctas ? segs : ctas), DH / 16 * NT);
   cfg.blockDim = dim3(kCombineThreads);

@@ -36,6 +36,7 @@ _NULL = contextlib.nullcontext()
 _pack = _lib.PAGED_CACHE.pack
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _FP16, _I32, _F32 = torch.float16, torch.int32, torch.float32
+_WS_BYTES = {}
 
 
 def _on(index: int):
@@ -186,7 +187,12 @@ def attention_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: t
         return y
     L = _lib.lib()
     with _on(index):
-        nbytes = L.tri_paged_attention_workspace_bytes(M, H, heads, dh) or 256
+        key = (M, H, heads, dh, index)
+        nbytes = _WS_BYTES.get(key)
+        if nbytes is None:
+            if len(_WS_BYTES) > 4096:
+                _WS_BYTES.clear()
+            nbytes = _WS_BYTES[key] = L.tri_paged_attention_workspace_bytes(M, H, heads, dh) or 256
         ws = workspace.get(nbytes) if workspace is not None else torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         if ws.get_device() != index:
             raise ValueError("the workspace must live on the tensors' device")
