@@ -23,7 +23,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _lib
+from . import _lib, paged
 from .api import PATH_AUTO, Workspace, _ptr, _require_cuda, _stream, gemm, gemm_swiglu, interleave_gate_up, pack
 
 HEAD_DIM = 128
@@ -108,11 +108,25 @@ class DecodeBlock:
     ``weights``: dict of trits (int8, on any device) and float32 scales
     (one per matrix or one per 256-block) for "qkv" [(H + 2 Hkv) 128][D],
     "o" [D][H 128], "gate", "up" [F][D], "down" [D][F]; and fp16 gains
-    "g_attn", "g_mlp" [D], "gq", "gk" [128]."""
+    "g_attn", "g_mlp" [D], "gq", "gk" [128].
+
+    The caches are contiguous, [M][Hkv][Lmax][128], or, with ``cache`` (a
+    ``paged.PagedCache`` that the blocks of a model share), pages of its
+    ``layer``: the M rows of a step are then any rows of its sequences, negative
+    positions padding.  ``cs`` replaces the rotary table of Lmax positions
+    (``paged.rope_table``: stretched angles, part of the head) and
+    ``interleaved`` its pairing, with ``cache`` only."""
 
     def __init__(self, weights: dict, D: int, H: int, Hkv: int, F: int, M: int, Lmax: int, device,
-                 fmt: str = "tq2", eps: float = RMS_EPS, theta: float = ROPE_THETA):
+                 fmt: str = "tq2", eps: float = RMS_EPS, theta: float = ROPE_THETA, cache: "paged.PagedCache" = None,
+                 layer: int = 0, cs: torch.Tensor = None, interleaved: bool = False):
         dev = torch.device(device)
+        if cache is None and (cs is not None or interleaved):
+            raise ValueError("a rotary table of one's own and interleaved pairs need a paged cache")
+        if cache is not None and (tuple(cache.pools.shape[3:4]) != (Hkv,) or cache.pools.shape[5] != HEAD_DIM or
+                                  not 0 <= layer < cache.layers):
+            raise ValueError("the cache must have this block's key/value heads, of 128, and its layer")
+        self.cache, self.layer, self.interleaved = cache, layer, interleaved
         self.D, self.H, self.Hkv, self.F, self.M, self.Lmax, self.fmt, self.eps = D, H, Hkv, F, M, Lmax, fmt, eps
         self.dev = dev
         packed = {}
@@ -125,9 +139,11 @@ class DecodeBlock:
         self.down = packed["down"]
         self.g_attn, self.g_mlp = weights["g_attn"].to(dev), weights["g_mlp"].to(dev)
         self.gq, self.gk = weights["gq"].to(dev), weights["gk"].to(dev)
-        self.kcache = torch.zeros(M, Hkv, Lmax, HEAD_DIM, dtype=torch.float16, device=dev)
-        self.vcache = torch.zeros_like(self.kcache)
-        self.cs = rope_table(Lmax, dev, theta)
+        self.kcache = self.vcache = None
+        if cache is None:
+            self.kcache = torch.zeros(M, Hkv, Lmax, HEAD_DIM, dtype=torch.float16, device=dev)
+            self.vcache = torch.zeros_like(self.kcache)
+        self.cs = cs if cs is not None else rope_table(Lmax, dev, theta)
         f16 = dict(dtype=torch.float16, device=dev)
         self.buf = {"xn": torch.empty(M, D, **f16), "qkv": torch.empty(M, (H + 2 * Hkv) * HEAD_DIM, **f16),
                     "q": torch.empty(M, H, HEAD_DIM, **f16), "attn": torch.empty(M, H * HEAD_DIM, **f16),
@@ -143,16 +159,31 @@ class DecodeBlock:
             n += qs.numel() * qs.element_size() + d.numel() * d.element_size()
         return n
 
-    def step(self, x: torch.Tensor, pos: torch.Tensor, max_len: int, path: int = PATH_AUTO) -> torch.Tensor:
+    def step(self, x: torch.Tensor, pos: torch.Tensor, max_len: int = None, path: int = PATH_AUTO,
+             seq: torch.Tensor = None) -> torch.Tensor:
         """One decode step: x [M][D] fp16 (the new tokens' residual stream),
-        pos [M] int32 device positions (< Lmax), max_len >= max(pos) + 1.
-        Returns the block output [M][D] (a buffer reused by the next step)."""
+        pos [M] int32 device positions (< Lmax), max_len >= max(pos) + 1 (which
+        a paged cache does not need).  seq [M] int32: the rows' sequences in a
+        paged cache, which must have room for the positions (without it row m is
+        sequence m).  Returns the block output [M][D] (a buffer reused by the
+        next step)."""
+        if self.cache is None and (max_len is None or seq is not None):
+            raise ValueError("contiguous caches need max_len and take no seq")
         b, H, Hkv, D, F = self.buf, self.H, self.Hkv, self.D, self.F
         rmsnorm(x, self.g_attn, eps=self.eps, out=b["xn"])
         gemm(b["xn"], *self.qkv, (H + 2 * Hkv) * HEAD_DIM, D, self.fmt, path=path, out=b["qkv"],
              workspace=self.ws["qkv"])
-        qknorm_rope(b["qkv"], pos, self.gq, self.gk, self.cs, self.kcache, self.vcache, H, Hkv, self.eps, out=b["q"])
-        attention_decode(b["q"], self.kcache, self.vcache, pos, max_len, workspace=self.ws["attn"], out=b["attn"])
+        if self.cache is not None:
+            k, v, ks, vs = self.cache.layer(self.layer)
+            table = self.cache.table
+            paged.qknorm_rope_append(b["qkv"], pos, self.gq, self.gk, self.cs, k, v, table, H, seq=seq,
+                                     interleaved=self.interleaved, k_scale=ks, v_scale=vs, eps=self.eps, out=b["q"])
+            paged.attention_decode(b["q"], k, v, table, pos, seq=seq, k_scale=ks, v_scale=vs, out=b["attn"],
+                                   workspace=self.ws["attn"])
+        else:
+            qknorm_rope(b["qkv"], pos, self.gq, self.gk, self.cs, self.kcache, self.vcache, H, Hkv, self.eps,
+                        out=b["q"])
+            attention_decode(b["q"], self.kcache, self.vcache, pos, max_len, workspace=self.ws["attn"], out=b["attn"])
         gemm(b["attn"], *self.o, D, H * HEAD_DIM, self.fmt, path=path, out=b["o"], workspace=self.ws["o"])
         rmsnorm(x, self.g_mlp, r=b["o"], eps=self.eps, out=b["hn"], h_out=b["h"])
         gemm_swiglu(b["hn"], *self.gu, F, D, self.fmt, path=path, out=b["f"], workspace=self.ws["gu"])

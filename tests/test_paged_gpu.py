@@ -549,3 +549,121 @@ def test_entry_points_refuse_bad_tensors():
         paged.copy_pages(k, [0], [4])
     with pytest.raises(ValueError):
         paged.copy_pages(k[:, :, :4], [0], [1])
+
+
+# ---------------------------------------------------------------- the ternary block on pages
+def _block_weights(Dm, F, H, Hkv, seed):
+    from bit_mixed_precision_tri_b200 import inputs
+    w = {}
+    shapes = {"qkv": ((H + 2 * Hkv) * 128, Dm), "o": (Dm, H * 128), "gate": (F, Dm), "up": (F, Dm), "down": (Dm, F)}
+    for i, (name, (n, k)) in enumerate(shapes.items()):
+        w[name] = (inputs.random_trits(n, k, 0.31, seed + i), torch.tensor([0.0159]))
+    rng = np.random.default_rng(seed)
+    for name, n in (("g_attn", Dm), ("g_mlp", Dm), ("gq", 128), ("gk", 128)):
+        w[name] = _t(D.rn16(rng.uniform(0.5, 1.5, n)))
+    return w
+
+
+@pytest.mark.parametrize("fmt", ["tq2", "tq1"])
+def test_block_on_pages_follows_the_contiguous_block(fmt):
+    """Twelve steps of three ragged sequences on both kinds of cache.  Each step's
+    attention and cache entries agree to one rounding each (2^-10 of the value);
+    what follows is the same arithmetic, so the outputs stay within the block's
+    own bound, 2^-9 of the value and of the row's size."""
+    Dm, F, H, Hkv, M = 512, 512, 4, 2, 3
+    w = _block_weights(Dm, F, H, Hkv, 3)
+    flat = dec.DecodeBlock(w, Dm, H, Hkv, F, M, 64, DEV, fmt=fmt)
+    cache = paged.PagedCache(30, Hkv, 5, 8, DEV, layers=2, page_size=8)
+    blk = dec.DecodeBlock(w, Dm, H, Hkv, F, M, 64, DEV, fmt=fmt, cache=cache, layer=1)
+    rng = np.random.default_rng(4)
+    start = [0, 5, 40]
+    seqs = [cache.new(n) for n in (0, 3, 0)]
+    cache.free(seqs[0])
+    seqs = [seqs[2], seqs[1], cache.new()]                    # handles that are not row numbers
+    cache.extend(seqs[1], 2)
+    cache.extend(seqs[2], 40)
+    k, v, _, _ = cache.layer(1)
+    for m, n in enumerate(start):                             # the same history in both
+        hist = torch.from_numpy(rng.standard_normal((2, Hkv, n, 128)).astype(np.float16)).to(DEV)
+        flat.kcache[m, :, :n], flat.vcache[m, :, :n] = hist[0], hist[1]
+        for p in range(n):
+            pg = int(cache.table[seqs[m], p // 8])
+            k[pg, :, p % 8], v[pg, :, p % 8] = hist[0, :, p], hist[1, :, p]
+    seq = _t(seqs, torch.int32)
+    for step in range(12):
+        x = _t(D.rn16(rng.standard_normal((M, Dm))))
+        pos = torch.tensor([n + step for n in start], dtype=torch.int32, device=DEV)
+        for s in seqs:
+            cache.extend(s)
+        a = _np(flat.step(x, pos, 64))
+        b = _np(blk.step(x, pos, seq=seq))
+        tol = 2.0 ** -9 * (np.abs(a) + np.sqrt(np.mean(a ** 2, -1, keepdims=True)))
+        assert np.all(np.abs(a - b) <= tol)
+        assert not torch.any(cache.pools[0])                  # the other layer is untouched
+
+
+def test_block_on_pages_captured_step_serves_growth_forks_and_padding():
+    """One captured step, replayed while sequences grow, fork, are dropped from
+    the batch and the pool is compacted, against the same steps run eagerly on a
+    cache of their own."""
+    Dm, F, H, Hkv, M = 512, 512, 4, 2, 4
+    w = _block_weights(Dm, F, H, Hkv, 5)
+    caches = [paged.PagedCache(40, Hkv, 6, 6, DEV, page_size=8, dtype=E4M3, k_scale=torch.full((Hkv,), 0.05),
+                               v_scale=torch.full((Hkv,), 0.02)) for _ in range(2)]
+    cs = paged.rope_table(48, DEV, rot=64, scaling="linear", factor=2.0)
+    blks = [dec.DecodeBlock(w, Dm, H, Hkv, F, M, 48, DEV, cache=c, cs=cs, interleaved=True) for c in caches]
+    x = torch.zeros(M, Dm, dtype=torch.float16, device=DEV)
+    pos = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+    seq = torch.zeros(M, dtype=torch.int32, device=DEV)
+    blks[0].step(x, pos, seq=seq)                             # first calls outside the capture
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        out = blks[0].step(x, pos, seq=seq)
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(6)
+    live = []
+    for c in caches:
+        a = c.new()
+        b = c.new()
+    live = [a, b]
+    for step in range(30):
+        if step == 10:
+            live.append([c.fork(live[0]) for c in caches][0])
+        if step == 17:
+            for c in caches:
+                c.free(live[1])
+            live.pop(1)
+            assert caches[0].compact() > 0                    # only one of the two is compacted
+        if step == 20:
+            for c in caches:
+                c.drop_front(live[0], 9)
+        for c in caches:
+            for h in live:
+                c.extend(h)
+        n = len(live)
+        x.copy_(_t(D.rn16(rng.standard_normal((M, Dm)))))
+        pos.copy_(torch.tensor([caches[0].length(h) - 1 for h in live] + [-1] * (M - n), dtype=torch.int32))
+        seq.copy_(torch.tensor(live + [0] * (M - n), dtype=torch.int32))
+        g.replay()
+        ref = blks[1].step(x, pos, seq=seq)
+        assert torch.equal(out[:n], ref[:n]), step
+        assert torch.all(torch.isfinite(out))
+
+
+def test_block_refuses_what_its_cache_cannot_serve():
+    w = _block_weights(512, 512, 4, 2, 7)
+    cache = paged.PagedCache(4, 2, 2, 2, DEV)
+    with pytest.raises(ValueError):
+        dec.DecodeBlock(w, 512, 4, 2, 512, 1, 16, DEV, cache=cache, layer=1)
+    with pytest.raises(ValueError):
+        dec.DecodeBlock(w, 512, 4, 4, 512, 1, 16, DEV, cache=cache)
+    with pytest.raises(ValueError):
+        dec.DecodeBlock(w, 512, 4, 2, 512, 1, 16, DEV, interleaved=True)
+    blk = dec.DecodeBlock(w, 512, 4, 2, 512, 1, 16, DEV)
+    x, pos = torch.zeros(1, 512, dtype=torch.float16, device=DEV), _t([0], torch.int32)
+    with pytest.raises(ValueError):
+        blk.step(x, pos)
+    with pytest.raises(ValueError):
+        blk.step(x, pos, 16, seq=pos)
