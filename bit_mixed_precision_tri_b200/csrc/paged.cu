@@ -180,7 +180,8 @@ struct Turner {
       float ss = s2.x + s2.y;
 #pragma unroll
       for (int d = LPH / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
-      rstd = rsqrtf(fmaf(ss, 1.f / (float)DH, eps));            // a few units of 2^-24
+      // off by a few units of 2^-24; its argument is 0 or at least 2^-55 (the smallest fp16 squared, / 128)
+      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rstd) : "f"(fmaf(ss, 1.f / (float)DH, eps)));
     }
     if (all) {
 #pragma unroll
@@ -509,8 +510,8 @@ cudaError_t launch_paged_qknorm_rope(const __half* qkv, int64_t qkv_stride, cons
   p.chunks = (int)ceil_div(nh, p.heads);
   p.blocks = ceil_div(T, p.rows);
   p.stage_bytes = (int)((p.rows * (p.heads * head_bytes + rot * 4) + 127) & ~int64_t(127));
-  // about four heads per group of lanes, and no group without a row
-  while ((1 << p.gpt_shift) < groups && ((4 << p.gpt_shift) < p.heads || (groups >> p.gpt_shift) > p.rows)) ++p.gpt_shift;
+  // as few groups of lanes per row (its coefficients are formed by each) as leave none without a row
+  while ((groups >> p.gpt_shift) > p.rows) ++p.gpt_shift;
   const int64_t items = p.blocks * p.chunks, most = 3 * (int64_t)sms;
   const int ctas = (int)(items < most ? items : most);
   p.next_block = ctas / p.chunks, p.next_chunk = ctas % p.chunks;
