@@ -540,7 +540,7 @@ cudaError_t launch_copy_pages(uint8_t* pools, int64_t n_pools, int64_t pool_stri
   const int64_t upp = ceil_div(page_bytes, kCopyUnit);
   const int64_t ctas = ceil_div(n * n_pools, 8) < (int64_t(1) << 40) / upp ? ceil_div(n * n_pools * upp, 8)
                                                                              : (int64_t(1) << 40);
-  const int64_t most = (int64_t)sms * 8;
+  const int64_t most = (int64_t)sms * 64;
   copy_pages_kernel<<<(unsigned)(ctas < most ? ctas : most), 256, 0, s>>>(
       pools, n_pools, pool_stride, (int)pages, page_stride, page_bytes, src, dst, n, upp);
   return cudaGetLastError();
