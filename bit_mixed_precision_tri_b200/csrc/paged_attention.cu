@@ -16,7 +16,7 @@
 //    128 bytes of each, hardware-swizzled), and the row's queries with the first
 //    tile.  Absent pages are not loaded.  A descriptor per stage says what the
 //    tile is.
-//  * Four consumer warps take 16 or 32 positions of a tile each.  Scores are formed
+//  * Four consumer warps (per 8 query heads) take 16 or 32 positions of a tile each.  Scores are formed
 //    transposed, S^T = K Q^T (mma.sync m16n8k16: positions are the 16 rows, up
 //    to 8 query heads the columns, so that no row is wasted on heads that do not
 //    exist), with the running maximum and sum in fp32 per warp.  O^T += V^T P^T:
@@ -36,33 +36,32 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWarps = 4;                    // consumer warps, 16 or 32 positions of a tile each
-constexpr int kThreads = 32 * (kWarps + 2);  // and two producer warps, of K and of V
 constexpr int kMaxStages = 8;
 constexpr int kSoloRun = 2;                  // a run of more tiles gives one-tile (row, head)s to single warps
 constexpr uint32_t kWaitPolls = 1u << 18;    // about a second
 constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
 
-template <int DH, bool FP8, int NT>
+// HG: groups of 8 query heads per key/value head, 1 or 2
+template <int DH, bool FP8, int HG>
 struct Cfg {
+  static constexpr int kWarps = 4 * HG;                       // consumer warps
+  static constexpr int kThreads = 32 * (kWarps + 2);          // and two producer warps, of K and of V
+  static constexpr int kCtasPerSm = HG == 2 ? 1 : 2;          // eight consumer warps per SM
   static constexpr int kRow = DH * (FP8 ? 1 : 2);             // bytes of a position
   // A warp's chain of dependent steps per tile (scores, maximum, weights, output)
   // takes about 0.7 us whatever its width, so rows of at most 128 bytes come 128 to
   // a tile (two sets of 16 per warp); 256-byte ones, for which HBM is slower than
-  // that chain, 64, and more than 8 query heads, two chains by themselves, too.
-  static constexpr int kSets = kRow <= 128 && NT == 1 ? 2 : 1;
+  // that chain, 64.
+  static constexpr int kSets = kRow <= 128 ? 2 : 1;
   static constexpr int kTile = 64 * kSets;                    // positions per stage
   static constexpr int kTileShift = kSets == 2 ? 7 : 6;
   static constexpr int kBox = kRow < 128 ? kRow : 128;        // bytes of it in one box
   static constexpr int kParts = kRow / kBox;
   static constexpr int kKV = kTile * kRow;                    // bytes of a K (or V) tile
   static constexpr int kQRow = DH * 2 + 16;                   // padded: fragment reads hit distinct banks
-  static constexpr int kQ = 8 * NT * kQRow;
-  static constexpr int kMerge = 2 * DH * 8 * NT * 4;          // two warps' outputs
-  // two CTAs per SM, except 16 query heads over 256-byte rows, whose three
-  // stages, queries and merge buffer do not fit twice
-  static constexpr int kCtasPerSm = NT == 2 && kRow == 256 ? 1 : 2;
-  static constexpr int kRoom = (kCtasPerSm == 1 ? 200 : 113) * 1024 - kMerge - 2560;
+  static constexpr int kQ = 8 * HG * kQRow;
+  static constexpr int kMerge = HG * 2 * DH * 8 * 4;          // two warps' outputs of each group
+  static constexpr int kRoom = (kCtasPerSm == 1 ? 224 : 113) * 1024 - kMerge - 2560;
   static constexpr int kFit = kRoom / (2 * kKV + kQ);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kSmem = 1024 + kStages * (2 * kKV + kQ) + kMerge;
@@ -84,8 +83,8 @@ struct Params {
   __half* out;
   int4* recs;                 // {row * heads + head, first CTA, partials (0: not split), -}, one per
                               // (row, head) where there are no more of them than CTAs, else per CTA
-  float2* ml;                 // [2 CTAs][8 NT] (max, sum)
-  float4* part;               // [2 CTAs][DH/16][NT][32 lanes]
+  float2* ml;                 // [2 CTAs][8 HG] (max, sum)
+  float4* part;               // [2 CTAs][DH/16][HG][32 lanes]
   unsigned* error;
   int64_t q_stride, out_stride, table_stride, M;
   int heads, G, page_shift, pages, seqs, max_len, ctas;
@@ -169,20 +168,21 @@ __device__ __forceinline__ void store_out(__half* dst, int h0, int G, int f, int
   }
 }
 
-template <int DH, bool FP8, int NT>
-__global__ void __launch_bounds__(kThreads, (Cfg<DH, FP8, NT>::kCtasPerSm))
+template <int DH, bool FP8, int HG>
+__global__ void __launch_bounds__((Cfg<DH, FP8, HG>::kThreads), (Cfg<DH, FP8, HG>::kCtasPerSm))
 paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const Params p) {
-  using C = Cfg<DH, FP8, NT>;
+  using C = Cfg<DH, FP8, HG>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads, kTile = C::kTile;
+  constexpr int kTileShift = C::kTileShift, kSets = C::kSets;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
   uint8_t* qring = sm + C::kStages * 2 * C::kKV;
   float4* merge = reinterpret_cast<float4*>(qring + C::kStages * C::kQ);
   __shared__ uint64_t full[C::kStages], empty[C::kStages];
   __shared__ Desc desc[C::kStages];
-  __shared__ float2 wml[kWarps][8 * NT];
+  __shared__ __align__(16) float2 wml[kWarps][8];
   __shared__ long long sums[kWarps + 2], s_first_prefix;
   __shared__ int s_first_row;
-  constexpr int kTile = C::kTile, kTileShift = C::kTileShift, kSets = C::kSets;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto row_tiles = [](int len) { return (len + kTile - 1) >> kTileShift; };
 
@@ -343,7 +343,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   }
 
   // -------------------------------------------------------------- consumers
-  const int gid = lane >> 2, tig = lane & 3;
+  const int gid = lane >> 2, tig = lane & 3, quarter = warp & 3, group = warp >> 2;
+  const int hb = 8 * group;                                     // the first of this warp's query heads
   const int page_shift = p.page_shift < kTileShift ? p.page_shift : kTileShift;
   // ldmatrix rows and 16-byte chunks: K (and e4m3 V): rows (lane & 7) + 8 (lane
   // >> 3 & 1), chunk + (lane >> 4); fp16 V transposed: rows (lane & 7) + 8 (lane
@@ -351,9 +352,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   const int r_a = (lane & 7) + 8 * ((lane >> 3) & 1), c_a = lane >> 4;
   const int r_t = (lane & 7) + 8 * (lane >> 4), c_t = (lane >> 3) & 1;
   auto address = [](uint32_t base, int row, int chunk) { return tile_address<C>(base, row, chunk); };
-  uint32_t qf[DH / 16][NT][2];
-  float o[DH / 16][NT][4];
-  float mx[NT][2], l[NT][2];
+  uint32_t qf[DH / 16][2];
+  float o[DH / 16][4];
+  float mx[2], l[2];
   float c2 = 0.f;
   uint32_t polls = kWaitPolls, phase = 0;
   int st = 0;
@@ -368,146 +369,125 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // a one-tile (row, head) in a longer run is one warp's, with no merge; its
     // neighbours are the other warps'
     const bool solo = d.flags & kSolo;
-    if (solo && (int)(i & (kWarps - 1)) != warp) {
+    if (solo && (int)(i & 3) != quarter) {
       if (lane == 0) mbar_arrive(&empty[st]);
       continue;
     }
     const uint32_t kbase = smem_u32(sm) + (uint32_t)(st * 2 * C::kKV), vbase = kbase + C::kKV;
     if (d.flags & kFirst) {
       const uint32_t qb = smem_u32(qring + st * C::kQ);
+      const bool real = hb + gid < p.G;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int hd = 8 * nt + gid;
-        const bool real = hd < p.G;
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          // fp16: features 2 tig, +1 and 8 + 2 tig, +1 of the step; e4m3: 4 tig .. 4 tig + 3,
-          // the order in which a lane gets its four bytes of K
-          const uint32_t a = qb + (uint32_t)(hd * C::kQRow + kk * 32 + (FP8 ? 8 : 4) * tig);
-          qf[kk][nt][0] = real ? lds32(a) : 0u;
-          qf[kk][nt][1] = real ? lds32(a + (FP8 ? 4 : 16)) : 0u;
-        }
-        mx[nt][0] = mx[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int fb = 0; fb < DH / 16; ++fb) o[fb][nt][0] = o[fb][nt][1] = o[fb][nt][2] = o[fb][nt][3] = 0.f;
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        // fp16: features 2 tig, +1 and 8 + 2 tig, +1 of the step; e4m3: 4 tig .. 4 tig + 3,
+        // the order in which a lane gets its four bytes of K
+        const uint32_t a = qb + (uint32_t)((hb + gid) * C::kQRow + kk * 32 + (FP8 ? 8 : 4) * tig);
+        qf[kk][0] = real ? lds32(a) : 0u;
+        qf[kk][1] = real ? lds32(a + (FP8 ? 4 : 16)) : 0u;
       }
+      mx[0] = mx[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+#pragma unroll
+      for (int fb = 0; fb < DH / 16; ++fb) o[fb][0] = o[fb][1] = o[fb][2] = o[fb][3] = 0.f;
       c2 = p.scale * 1.4426950408889634f * (FP8 ? p.k_scale[d.head] : 1.f);
     }
     // blocks of 16 kSets positions: this warp's, or all; none past the row's end,
     // none where nothing was loaded
     const int blocks = d.pages == 0 ? 0 : (d.nval + 16 * kSets - 1) / (16 * kSets);
-    const int blk_end = solo ? blocks : (warp < blocks ? warp + 1 : 0);
-    for (int blk = solo ? 0 : warp; blk < blk_end; ++blk) {
-    const int r0 = 16 * kSets * blk;
-    // ---- S^T = K Q^T
-    float sc[kSets][NT][4];
-    if constexpr (kSets == 1 && !FP8) {                          // two chains of dependent MMAs
-      float odd[NT][4];
+    const int blk_end = solo ? blocks : (quarter < blocks ? quarter + 1 : 0);
+    for (int blk = solo ? 0 : quarter; blk < blk_end; ++blk) {
+      const int r0 = 16 * kSets * blk;
+      // ---- S^T = K Q^T
+      float sc[kSets][4];
+      if constexpr (kSets == 1 && !FP8) {                          // two chains of dependent MMAs
+        float odd[4] = {};
+        sc[0][0] = sc[0][1] = sc[0][2] = sc[0][3] = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          uint32_t a[4];
+          ldsm_x4(address(kbase, r0 + r_a, 2 * kk + c_a), a);
+          mma_16816(kk & 1 ? odd : sc[0], a, qf[kk][0], qf[kk][1]);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[0][nt][e] = odd[nt][e] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < DH / 16; ++kk) {
-        uint32_t a[4];
-        ldsm_x4(address(kbase, r0 + r_a, 2 * kk + c_a), a);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816(kk & 1 ? odd[nt] : sc[0][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[0][nt][e] += odd[nt][e];
-    } else {
-#pragma unroll
-      for (int u = 0; u < kSets; ++u)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[u][nt][e] = 0.f;
-      if constexpr (FP8) {
-#pragma unroll
-        for (int kp = 0; kp < DH / 32; ++kp)
-#pragma unroll
-          for (int u = 0; u < kSets; ++u) {
-            uint32_t r[4];
-            ldsm_x4(address(kbase, r0 + r_a + 16 * u, 2 * kp + c_a), r);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t a[4];
-              e4m3x4_to_half2(r[2 * k], a[0], a[2]);
-              e4m3x4_to_half2(r[2 * k + 1], a[1], a[3]);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_16816(sc[u][nt], a, qf[2 * kp + k][nt][0], qf[2 * kp + k][nt][1]);
-            }
-          }
+        for (int e = 0; e < 4; ++e) sc[0][e] += odd[e];
       } else {
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
+        for (int u = 0; u < kSets; ++u) sc[u][0] = sc[u][1] = sc[u][2] = sc[u][3] = 0.f;
+        if constexpr (FP8) {
 #pragma unroll
-          for (int u = 0; u < kSets; ++u) {
-            uint32_t a[4];
-            ldsm_x4(address(kbase, r0 + r_a + 16 * u, 2 * kk + c_a), a);
+          for (int kp = 0; kp < DH / 32; ++kp)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816(sc[u][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
-          }
-      }
-    }
-    // ---- positions that do not count (behind the row's end, in absent pages): no
-    // weight, and a weight of zero times a NaN would be NaN, so their V rows are
-    // cleared in the stage before they are read
-    if (d.nval != kTile || d.pages != (1 << (kTile >> page_shift)) - 1) {
-      auto valid = [&](int r) { return r < d.nval && ((d.pages >> (r >> page_shift)) & 1); };
+            for (int u = 0; u < kSets; ++u) {
+              uint32_t r[4];
+              ldsm_x4(address(kbase, r0 + r_a + 16 * u, 2 * kp + c_a), r);
 #pragma unroll
-      for (int u = 0; u < kSets; ++u) {
-        const int set = r0 + 16 * u;
-        const bool v0 = valid(set + gid), v1 = valid(set + gid + 8);
+              for (int k = 0; k < 2; ++k) {
+                uint32_t a[4];
+                e4m3x4_to_half2(r[2 * k], a[0], a[2]);
+                e4m3x4_to_half2(r[2 * k + 1], a[1], a[3]);
+                mma_16816(sc[u], a, qf[2 * kp + k][0], qf[2 * kp + k][1]);
+              }
+            }
+        } else {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (!v0) sc[u][nt][0] = sc[u][nt][1] = -INFINITY;
-          if (!v1) sc[u][nt][2] = sc[u][nt][3] = -INFINITY;
+          for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+            for (int u = 0; u < kSets; ++u) {
+              uint32_t a[4];
+              ldsm_x4(address(kbase, r0 + r_a + 16 * u, 2 * kk + c_a), a);
+              mma_16816(sc[u], a, qf[kk][0], qf[kk][1]);
+            }
         }
-        const int r = set + (lane >> 1);                         // two lanes a row
-        if (!valid(r))
-#pragma unroll
-          for (int c = 0; c < C::kRow / 32; ++c) {
-            const uint32_t a = address(vbase, r, 2 * c + (lane & 1));
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
-          }
       }
-      fence_proxy_async();                                       // before TMA refills the stage
-      __syncwarp();
-    }
-    // ---- running softmax; the eight lanes of a column hold the positions of a set
-    uint32_t ph[kSets][NT][2], pl[kSets][NT][2];
-    bool grew = false;
-    float alpha[NT][2];
+      // ---- positions that do not count (behind the row's end, in absent pages): no
+      // weight, and a weight of zero times a NaN would be NaN, so their V rows are
+      // cleared in the stage before they are read
+      if (d.nval != kTile || d.pages != (1 << (kTile >> page_shift)) - 1) {
+        auto valid = [&](int r) { return r < d.nval && ((d.pages >> (r >> page_shift)) & 1); };
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+        for (int u = 0; u < kSets; ++u) {
+          const int set = r0 + 16 * u;
+          const bool v0 = valid(set + gid), v1 = valid(set + gid + 8);
+          if (!v0) sc[u][0] = sc[u][1] = -INFINITY;
+          if (!v1) sc[u][2] = sc[u][3] = -INFINITY;
+          const int r = set + (lane >> 1);                         // two lanes a row
+          if (!valid(r))
+#pragma unroll
+            for (int c = 0; c < C::kRow / 32; ++c) {
+              const uint32_t a = address(vbase, r, 2 * c + (lane & 1));
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+            }
+        }
+        fence_proxy_async();                                       // before TMA refills the stage
+        __syncwarp();
+      }
+      // ---- running softmax; the eight lanes of a column hold the positions of a set
+      uint32_t ph[kSets][2], pl[kSets][2];
+      bool grew = false;
+      float alpha[2];
       float pr[kSets][4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float top = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
+        float top = fmaxf(sc[0][e], sc[0][2 + e]);
 #pragma unroll
-        for (int u = 1; u < kSets; ++u) top = fmaxf(top, fmaxf(sc[u][nt][e], sc[u][nt][2 + e]));
+        for (int u = 1; u < kSets; ++u) top = fmaxf(top, fmaxf(sc[u][e], sc[u][2 + e]));
         top *= c2;
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        const float mnew = fmaxf(mx[nt][e], top);
+        const float mnew = fmaxf(mx[e], top);
         const float base = mnew == -INFINITY ? 0.f : mnew;       // nothing seen yet: all weights 0
-        alpha[nt][e] = ex2(mx[nt][e] - base);
-        grew |= mnew > mx[nt][e];
-        mx[nt][e] = mnew;
+        alpha[e] = ex2(mx[e] - base);
+        grew |= mnew > mx[e];
+        mx[e] = mnew;
         float sum = 0.f;
 #pragma unroll
         for (int u = 0; u < kSets; ++u) {
-          pr[u][e] = ex2(fmaf(sc[u][nt][e], c2, -base));
-          pr[u][2 + e] = ex2(fmaf(sc[u][nt][2 + e], c2, -base));
+          pr[u][e] = ex2(fmaf(sc[u][e], c2, -base));
+          pr[u][2 + e] = ex2(fmaf(sc[u][2 + e], c2, -base));
           sum += pr[u][e] + pr[u][2 + e];
         }
-        l[nt][e] = fmaf(l[nt][e], alpha[nt][e], sum);
+        l[e] = fmaf(l[e], alpha[e], sum);
       }
 #pragma unroll
       for (int u = 0; u < kSets; ++u)
@@ -515,54 +495,45 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (int r = 0; r < 2; ++r) {
           const uint32_t hi = half2_bits(pr[u][2 * r], pr[u][2 * r + 1]);
           const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          pl[u][nt][r] = transpose8x8(half2_bits(pr[u][2 * r] - h.x, pr[u][2 * r + 1] - h.y));
-          ph[u][nt][r] = transpose8x8(hi);
+          pl[u][r] = transpose8x8(half2_bits(pr[u][2 * r] - h.x, pr[u][2 * r + 1] - h.y));
+          ph[u][r] = transpose8x8(hi);
         }
-    }
-    if (__any_sync(0xFFFFFFFFu, grew)) {                         // rare after the first tiles
+      if (__any_sync(0xFFFFFFFFu, grew)) {                         // rare after the first tiles
 #pragma unroll
-      for (int fb = 0; fb < DH / 16; ++fb)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          o[fb][nt][0] *= alpha[nt][0], o[fb][nt][1] *= alpha[nt][1];
-          o[fb][nt][2] *= alpha[nt][0], o[fb][nt][3] *= alpha[nt][1];
+        for (int fb = 0; fb < DH / 16; ++fb) {
+          o[fb][0] *= alpha[0], o[fb][1] *= alpha[1];
+          o[fb][2] *= alpha[0], o[fb][3] *= alpha[1];
         }
-    }
-    // ---- O^T += V^T P^T
-    if constexpr (FP8) {
+      }
+      // ---- O^T += V^T P^T
+      if constexpr (FP8) {
 #pragma unroll
-      for (int fp = 0; fp < DH / 32; ++fp)
+        for (int fp = 0; fp < DH / 32; ++fp)
 #pragma unroll
-        for (int u = 0; u < kSets; ++u) {
-          uint32_t r[4];
-          ldsm_x4_t(address(vbase, r0 + r_a + 16 * u, 2 * fp + c_a), r);
+          for (int u = 0; u < kSets; ++u) {
+            uint32_t r[4];
+            ldsm_x4_t(address(vbase, r0 + r_a + 16 * u, 2 * fp + c_a), r);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            // bytes: position 2 tig, features 2 gid and 2 gid + 1; position 2 tig + 1, the same
-            uint32_t a[4];
-            e4m3x4_to_half2(__byte_perm(r[2 * k], 0, 0x3120), a[0], a[1]);
-            e4m3x4_to_half2(__byte_perm(r[2 * k + 1], 0, 0x3120), a[2], a[3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_16816(o[2 * fp + k][nt], a, ph[u][nt][0], ph[u][nt][1]);
-              mma_16816(o[2 * fp + k][nt], a, pl[u][nt][0], pl[u][nt][1]);
+            for (int k = 0; k < 2; ++k) {
+              // bytes: position 2 tig, features 2 gid and 2 gid + 1; position 2 tig + 1, the same
+              uint32_t a[4];
+              e4m3x4_to_half2(__byte_perm(r[2 * k], 0, 0x3120), a[0], a[1]);
+              e4m3x4_to_half2(__byte_perm(r[2 * k + 1], 0, 0x3120), a[2], a[3]);
+              mma_16816(o[2 * fp + k], a, ph[u][0], ph[u][1]);
+              mma_16816(o[2 * fp + k], a, pl[u][0], pl[u][1]);
             }
           }
-        }
-    } else {
+      } else {
 #pragma unroll
-      for (int fb = 0; fb < DH / 16; ++fb)
+        for (int fb = 0; fb < DH / 16; ++fb)
 #pragma unroll
-        for (int u = 0; u < kSets; ++u) {
-          uint32_t a[4];
-          ldsm_x4_t(address(vbase, r0 + r_t + 16 * u, 2 * fb + c_t), a);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_16816(o[fb][nt], a, ph[u][nt][0], ph[u][nt][1]);
-            mma_16816(o[fb][nt], a, pl[u][nt][0], pl[u][nt][1]);
+          for (int u = 0; u < kSets; ++u) {
+            uint32_t a[4];
+            ldsm_x4_t(address(vbase, r0 + r_t + 16 * u, 2 * fb + c_t), a);
+            mma_16816(o[fb], a, ph[u][0], ph[u][1]);
+            mma_16816(o[fb], a, pl[u][0], pl[u][1]);
           }
-        }
-    }
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
@@ -570,102 +541,70 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
     const float vs = FP8 ? p.v_scale[d.head] : 1.f;
     __half* dst = p.out + (int64_t)d.row * p.out_stride + (int64_t)d.head * p.G * DH;
+    const int h0 = hb + 2 * tig;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 4);
+      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 8);
+      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 16);
+    }
     if (solo) {
+      const float i0 = l[0] == 0.f ? 0.f : vs / l[0], i1 = l[1] == 0.f ? 0.f : vs / l[1];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float i2[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = l[nt][e];
-          v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
-          v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-          v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
-          i2[e] = v == 0.f ? 0.f : vs / v;
-        }
-#pragma unroll
-        for (int fb = 0; fb < DH / 16; ++fb)
-          store_out<DH, FP8>(dst, 8 * nt + 2 * tig, p.G, 16 * fb, gid,
-                             make_float4(o[fb][nt][0], o[fb][nt][1], o[fb][nt][2], o[fb][nt][3]), i2[0], i2[1]);
-      }
+      for (int fb = 0; fb < DH / 16; ++fb)
+        store_out<DH, FP8>(dst, h0, p.G, 16 * fb, gid, make_float4(o[fb][0], o[fb][1], o[fb][2], o[fb][3]), i0, i1);
       continue;
     }
-    // ---- the four warps' (max, sum, output) into one, in warp order
-    float f[NT][2], lsum[NT][2], mtop[NT][2];
+    // ---- the four quarters' (max, sum, output) into one, in their order; each
+    // group of four warps (8 query heads) by itself
+    float lsum[2], mtop[2];
+    if (gid == 0)
+      *reinterpret_cast<float4*>(&wml[warp][2 * tig]) = make_float4(mx[0], l[0], mx[1], l[1]);
+    named_bar_sync(1 + group, 128);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int e = 0; e < 2; ++e) {
+      float2 w[4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = l[nt][e];
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
-        if (gid == 0) wml[warp][8 * nt + 2 * tig + e] = make_float2(mx[nt][e], v);
-      }
-    named_bar_sync(1, 32 * kWarps);
+      for (int k = 0; k < 4; ++k) w[k] = wml[4 * group + k][2 * tig + e];
+      mtop[e] = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
+      const float base = mtop[e] == -INFINITY ? 0.f : mtop[e];
+      lsum[e] = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int k = 0; k < 4; ++k) lsum[e] = fmaf(w[k].y, ex2(w[k].x - base), lsum[e]);
+      const float f = ex2(mx[e] - base);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int hd = 8 * nt + 2 * tig + e;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, wml[w][hd].x);
-        const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum = fmaf(wml[w][hd].y, ex2(wml[w][hd].x - base), sum);
-        f[nt][e] = ex2(mx[nt][e] - base);
-        lsum[nt][e] = sum;
-        mtop[nt][e] = top;
-      }
-#pragma unroll
-    for (int fb = 0; fb < DH / 16; ++fb)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        o[fb][nt][0] *= f[nt][0], o[fb][nt][1] *= f[nt][1];
-        o[fb][nt][2] *= f[nt][0], o[fb][nt][3] *= f[nt][1];
-      }
-    constexpr int kVec = DH / 16 * NT * 32;                      // float4s of one warp's output
-    auto put = [&](float4* dst) {
-#pragma unroll
-      for (int fb = 0; fb < DH / 16; ++fb)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          dst[(fb * NT + nt) * 32 + lane] = make_float4(o[fb][nt][0], o[fb][nt][1], o[fb][nt][2], o[fb][nt][3]);
-    };
-    if (warp >= 2) put(merge + (warp - 2) * kVec);
-    named_bar_sync(1, 32 * kWarps);
-    if (warp < 2) {
-#pragma unroll
-      for (int fb = 0; fb < DH / 16; ++fb)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float4 v = merge[warp * kVec + (fb * NT + nt) * 32 + lane];
-          o[fb][nt][0] += v.x, o[fb][nt][1] += v.y, o[fb][nt][2] += v.z, o[fb][nt][3] += v.w;
-        }
-      put(merge + warp * kVec);
+      for (int fb = 0; fb < DH / 16; ++fb) o[fb][e] *= f, o[fb][2 + e] *= f;
     }
-    named_bar_sync(1, 32 * kWarps);
+    constexpr int kVec = DH / 16 * 32;                           // float4s of one warp's output
+    float4* buf = merge + group * 2 * kVec;
+    auto put = [&](float4* to) {
+#pragma unroll
+      for (int fb = 0; fb < DH / 16; ++fb) to[fb * 32 + lane] = make_float4(o[fb][0], o[fb][1], o[fb][2], o[fb][3]);
+    };
+    if (quarter >= 2) put(buf + (quarter - 2) * kVec);
+    named_bar_sync(1 + group, 128);
+    if (quarter < 2) {
+#pragma unroll
+      for (int fb = 0; fb < DH / 16; ++fb) {
+        const float4 v = buf[quarter * kVec + fb * 32 + lane];
+        o[fb][0] += v.x, o[fb][1] += v.y, o[fb][2] += v.z, o[fb][3] += v.w;
+      }
+      put(buf + quarter * kVec);
+    }
+    named_bar_sync(1 + group, 128);
     // every warp adds and stores a quarter of the features
     const bool open = d.flags & (kOpenLeft | kOpenRight);
     const int64_t slot = 2 * (int64_t)blockIdx.x + ((d.flags & kOpenLeft) ? 0 : 1);
+    if (open && quarter == 0 && gid == 0)
+      *reinterpret_cast<float4*>(&p.ml[slot * 8 * HG + h0]) = make_float4(mtop[0], lsum[0], mtop[1], lsum[1]);
+    const float i0 = lsum[0] == 0.f ? 0.f : vs / lsum[0], i1 = lsum[1] == 0.f ? 0.f : vs / lsum[1];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int h0 = 8 * nt + 2 * tig;
-      if (open && warp == 0 && gid == 0) {
-        p.ml[slot * 8 * NT + h0] = make_float2(mtop[nt][0], lsum[nt][0]);
-        p.ml[slot * 8 * NT + h0 + 1] = make_float2(mtop[nt][1], lsum[nt][1]);
-      }
-      const float i0 = lsum[nt][0] == 0.f ? 0.f : vs / lsum[nt][0];
-      const float i1 = lsum[nt][1] == 0.f ? 0.f : vs / lsum[nt][1];
-#pragma unroll
-      for (int b = 0; b < DH / 64; ++b) {
-        const int fb = warp * (DH / 64) + b, at = (fb * NT + nt) * 32 + lane;
-        const float4 u = merge[at], v = merge[kVec + at];
-        const float4 y = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
-        if (open) p.part[slot * kVec + at] = y;
-        else store_out<DH, FP8>(dst, h0, p.G, 16 * fb, gid, y, i0, i1);
-      }
+    for (int b = 0; b < DH / 64; ++b) {
+      const int fb = quarter * (DH / 64) + b;
+      const float4 u = buf[fb * 32 + lane], v = buf[kVec + fb * 32 + lane];
+      const float4 y = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+      if (open) p.part[slot * HG * kVec + (fb * HG + group) * 32 + lane] = y;
+      else store_out<DH, FP8>(dst, h0, p.G, 16 * fb, gid, y, i0, i1);
     }
   }
 }
@@ -678,13 +617,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 // order.
 constexpr int kCombineThreads = 256;
 
-template <int DH, bool FP8, int NT>
+template <int DH, bool FP8, int HG>
 __global__ void __launch_bounds__(kCombineThreads)
 paged_combine_kernel(const Params p) {
   extern __shared__ float wts[];                                 // [partials][8]
   __shared__ float inv[8];
   __shared__ float4 sums[8][32];
-  constexpr int kVec = DH / 16 * NT * 32;
+  constexpr int kVec = DH / 16 * HG * 32;
   griddep_wait();                                                // in every CTA: the grid ends after its predecessor
   const int4 rec = p.recs[blockIdx.x];
   const int J = rec.z;
@@ -692,7 +631,7 @@ paged_combine_kernel(const Params p) {
   if (J <= 0 || rec.y < 0 || J > p.ctas - rec.y || rec.x < 0 || rec.x >= p.M * p.heads) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = rec.x / p.heads, head = rec.x % p.heads;
-  const int vec = blockIdx.y * 32 + lane, fb = blockIdx.y / NT, nt = blockIdx.y % NT;
+  const int vec = blockIdx.y * 32 + lane, fb = blockIdx.y / HG, nt = blockIdx.y % HG;
   auto slot = [&](int j) -> int64_t { return 2 * (int64_t)(rec.y + j) + (j == 0 ? 1 : 0); };
   float4 v[4];
 #pragma unroll
@@ -700,15 +639,15 @@ paged_combine_kernel(const Params p) {
     if (warp + 8 * k < J) v[k] = p.part[slot(warp + 8 * k) * kVec + vec];
   {
     const float2* ml = p.ml + 8 * nt + warp;
-    const float2 none = make_float2(-INFINITY, 0.f), first = lane < J ? ml[slot(lane) * 8 * NT] : none;
+    const float2 none = make_float2(-INFINITY, 0.f), first = lane < J ? ml[slot(lane) * 8 * HG] : none;
     float top = first.x;
-    for (int j = lane + 32; j < J; j += 32) top = fmaxf(top, ml[slot(j) * 8 * NT].x);
+    for (int j = lane + 32; j < J; j += 32) top = fmaxf(top, ml[slot(j) * 8 * HG].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
     for (int j = lane; j < J; j += 32) {
-      const float2 u = j == lane ? first : ml[slot(j) * 8 * NT];
+      const float2 u = j == lane ? first : ml[slot(j) * 8 * HG];
       const float w = ex2(u.x - base);
       wts[j * 8 + warp] = w;
       sum = fmaf(w, u.y, sum);
@@ -764,17 +703,17 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 struct Space {
   size_t ml, part, total;
 };
-Space space(int64_t ctas, int64_t nt, int64_t dh) {
+Space space(int64_t ctas, int64_t hg, int64_t dh) {
   Space w;
   w.ml = up256((size_t)ctas * sizeof(int4));
-  w.part = w.ml + up256((size_t)(2 * ctas * 8 * nt) * sizeof(float2));
-  w.total = w.part + (size_t)(2 * ctas * 8 * nt * dh) * sizeof(float);
+  w.part = w.ml + up256((size_t)(2 * ctas * 8 * hg) * sizeof(float2));
+  w.total = w.part + (size_t)(2 * ctas * 8 * hg * dh) * sizeof(float);
   return w;
 }
 
-template <int DH, bool FP8, int NT>
+template <int DH, bool FP8, int HG>
 cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaStream_t s) {
-  using K = Cfg<DH, FP8, NT>;
+  using K = Cfg<DH, FP8, HG>;
   auto enc = encode_fn_p();
   if (!enc) return cudaErrorNotSupported;
   CUtensorMap maps[2];
@@ -796,7 +735,7 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<DH, FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
+    e = cudaFuncSetAttribute(paged_attn_kernel<DH, FP8, HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
@@ -804,13 +743,13 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
   const int64_t most = p.M * p.heads * (int64_t)((p.max_len + K::kTile - 1) / K::kTile);
   const int64_t ctas = most < (int64_t)K::kCtasPerSm * sms ? most : (int64_t)K::kCtasPerSm * sms;
   p.ctas = (int)ctas;
-  const Space w = space(ctas, NT, DH);
+  const Space w = space(ctas, HG, DH);
   p.recs = static_cast<int4*>(ws);
   p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + w.ml);
   p.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + w.part);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(K::kThreads);
   cfg.dynamicSmemBytes = K::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -818,13 +757,13 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<DH, FP8, NT>, maps[0], maps[1], p)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<DH, FP8, HG>, maps[0], maps[1], p)) != cudaSuccess) return e;
   if (p.max_len <= K::kTile) return cudaSuccess;                 // one tile a row at most: nothing is split
   const int64_t segs = p.M * p.heads;
-  cfg.gridDim = dim3((unsigned)(segs < ctas ? segs : ctas), DH / 16 * NT);
+  cfg.gridDim = dim3((unsigned)(segs < ctas ? segs : ctas), DH / 16 * HG);
   cfg.blockDim = dim3(kCombineThreads);
   cfg.dynamicSmemBytes = (size_t)ctas * 8 * sizeof(float);
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<DH, FP8, NT>, p);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<DH, FP8, HG>, p);
 }
 
 }  // namespace
