@@ -361,7 +361,8 @@ paged_append_stream_kernel(const AppendParams p) {
   uint32_t phase = 0;
   for (Item item(p); item.block < p.blocks; item.next(p), ++st) {
     if (st == kAppendStages) st = 0, phase ^= 1;
-    if (!mbar_wait(&full[st], phase, polls)) {
+    const bool arrived = mbar_wait(&full[st], phase, polls);
+    if (!arrived) {                                             // nothing of the item is stored
       if (lane == 0) record_wait_failure(p.error, kAppendConsumerCode);
       polls = 1;
     }
@@ -375,8 +376,8 @@ paged_append_stream_kernel(const AppendParams p) {
     const int gk = nq + ((gi - nq) & (gpt - 1)), gv = nqk + ((gi - nqk) & (gpt - 1));
     const uint8_t* stage = sm + st * p.stage_bytes;
     for (int r0 = 0; r0 < p.rows; r0 += per_pass) {             // shuffles below: trip counts are the CTA's
-      const bool real = r0 + gr < p.rows;
-      const int r = real ? r0 + gr : p.rows - 1;
+      const bool real = arrived && r0 + gr < p.rows;
+      const int r = r0 + gr < p.rows ? r0 + gr : p.rows - 1;
       const int2 at = place[st][r];
       const bool valid = real && at.x >= 0;
       const __half* src = reinterpret_cast<const __half*>(stage) + r * p.heads * DH;

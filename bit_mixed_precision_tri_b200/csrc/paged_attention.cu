@@ -21,8 +21,7 @@
 //    to 8 query heads the columns, so that no row is wasted on heads that do not
 //    exist), with the running maximum and sum in fp32 per warp.  O^T += V^T P^T:
 //    V^T comes from ldmatrix.trans, P^T from the S^T accumulators by movmatrix,
-//    in two fp16 parts (the weight and its rounding error), so that the fp32
-//    accumulation bounds the error.  e4m3 elements become fp16 (exactly) in
+//    in two fp16 parts, so that the fp32 accumulation bounds the error.  e4m3 elements become fp16 (exactly) in
 //    registers; the K scale joins the softmax scale, the V scale the output.
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -38,6 +37,10 @@ using namespace ptx;
 
 constexpr int kMaxStages = 8;
 constexpr int kSoloRun = 2;                  // a run of more tiles gives one-tile (row, head)s to single warps
+// Weights are held times 2^14, sums and outputs with them: the two fp16 parts then
+// reach down to 2^-38 of the largest weight instead of 2^-24, below which a hundred
+// thousand small weights would vanish from the output but not from their sum.
+constexpr float kWeightShift = 14.f;
 constexpr uint32_t kWaitPolls = 1u << 18;    // about a second
 constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
 
@@ -109,9 +112,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Two weights as two fp16 parts each, both at least the smallest fp16 (2^-38 of the
+// largest weight, see kWeightShift): with parts of one sign, neither of them 0, an
+// infinite value stays infinite.  The high part is rounded down, the low one is the
+// rest to 2^-21 of the weight.  A NaN stays one.
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 least = __halves2half2(__ushort_as_half(1), __ushort_as_half(1));
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+  const __half2 h = __hmax2_nan(*reinterpret_cast<const __half2*>(&hi), least);
+  const float2 f = __half22float2(h);
+  const __half2 g = __hmax2_nan(__floats2half2_rn(a - f.x, b - f.y), least);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&g);
 }
 // four e4m3 codes as fp16: bytes 0, 1 and bytes 2, 3
 __device__ __forceinline__ void e4m3x4_to_half2(uint32_t four, uint32_t& lo, uint32_t& hi) {
@@ -190,6 +202,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 2);
       mbar_init(&empty[s], kWarps);
+      desc[s] = Desc{};                                          // in range whatever becomes of a wait
     }
     fence_mbar_init();
   }
@@ -476,8 +489,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
         const float mnew = fmaxf(mx[e], top);
-        const float base = mnew == -INFINITY ? 0.f : mnew;       // nothing seen yet: all weights 0
-        alpha[e] = ex2(mx[e] - base);
+        const float top_seen = mnew == -INFINITY ? 0.f : mnew;   // nothing seen yet: all weights 0
+        const float base = top_seen - kWeightShift;
+        alpha[e] = ex2(mx[e] - top_seen);
         grew |= mnew > mx[e];
         mx[e] = mnew;
         float sum = 0.f;
@@ -493,9 +507,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       for (int u = 0; u < kSets; ++u)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t hi = half2_bits(pr[u][2 * r], pr[u][2 * r + 1]);
-          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          pl[u][r] = transpose8x8(half2_bits(pr[u][2 * r] - h.x, pr[u][2 * r + 1] - h.y));
+          uint32_t hi, lo;
+          split_weights(pr[u][2 * r], pr[u][2 * r + 1], hi, lo);
+          pl[u][r] = transpose8x8(lo);
           ph[u][r] = transpose8x8(hi);
         }
       if (__any_sync(0xFFFFFFFFu, grew)) {                         // rare after the first tiles

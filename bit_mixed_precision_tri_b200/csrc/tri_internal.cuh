@@ -107,7 +107,8 @@ cudaError_t launch_gemm_tc(int fmt, const __half* X, const uint8_t* qs, const __
 
 // ---- device wait status (status.cu) ----------------------------------------
 // codes recorded by a bounded wait that ran out; the values name the wait:
-// 1-2 gemv_mma.cu, 11 gemv_i8.cu, 21-26 gemm_tc.cu, 41-42 gemv_i8n.cu
+// 1-2 gemv_mma.cu, 11 gemv_i8.cu, 21-26 gemm_tc.cu, 41-42 gemv_i8n.cu,
+// 51-53 paged_attention.cu, 61-63 paged.cu
 constexpr unsigned kSelfTestMbarCode = 90;
 constexpr unsigned kSelfTestStampCode = 91;
 // the current device's status word (device address)

@@ -259,7 +259,7 @@ TRI_API tri_status tri_gemm_swiglu(int format, int path, const uint16_t* X, cons
                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
- * Device wait status.  The GEMM kernels wait on asynchronous copies, on the
+ * Device wait status.  The GEMM and paged kernels wait on asynchronous copies, on the
  * tensor-core pipeline and on partial sums of other thread blocks; each such
  * wait gives up after an iteration limit far beyond any wait a healthy call
  * sees (a second or more).  A wait that gives up stores a non-zero code in a
@@ -267,7 +267,8 @@ TRI_API tri_status tri_gemm_swiglu(int format, int path, const uint16_t* X, cons
  * cleared; later ones are dropped), lets the kernel drain and return, and
  * leaves that call's output unspecified.  Codes name the wait: 1-2 and 11
  * the decode kernels (M <= 2), 41-42 the integer kernel for 3 <= M <= 16,
- * 21-26 the tcgen05 kernel (M > 16), 90-91 tri_selftest_wait_timeout.
+ * 21-26 the tcgen05 kernel (M > 16), 51-53 the paged attention, 61-63 the paged
+ * append, 90-91 tri_selftest_wait_timeout.
  *
  * tri_wait_status: reads the current device's word in `stream` order (after
  *   the work already enqueued there), zeroes it there if `clear` is

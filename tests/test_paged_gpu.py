@@ -312,6 +312,71 @@ def test_attention_scale_and_large_scores():
     assert abs(float(o[0, 3]) - 24.5) <= 2.0 ** -11 * 24.5 and float(o[0, 4]) == 0.0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_many_tiny_weights_are_not_lost(fp8):
+    """One position outweighs 30000 others by e^17.5 each (2^-25.2 of its weight):
+    together they are a thousandth of the output."""
+    n, dh = 30001, 64
+    k = np.zeros((n, dh), np.float32)
+    v = np.zeros((n, dh), np.float32)
+    k[777, 0], v[:, 1], v[777, 1] = 17.5, 1.0, 0.0
+    pages = -(-n // 256)
+    pool = lambda a: torch.from_numpy(np.pad(a, ((0, pages * 256 - n), (0, 0))).reshape(pages, 1, 256, dh))
+    q = np.zeros((1, 1, dh))
+    q[0, 0, 0] = 1.0
+    if fp8:
+        k[777, 0] = 8.75
+        one, two = torch.ones(1, device=DEV), torch.full((1,), 2.0, device=DEV)
+        K, V, kw = pool(k).to(E4M3), pool(v).to(E4M3), dict(k_scale=two, v_scale=one)
+    else:
+        K, V, kw = pool(k).half(), pool(v).half(), {}
+    kr, vr = K.float().numpy().astype(np.float64) * (2 if fp8 else 1), V.float().numpy().astype(np.float64)
+    table, pos = np.arange(pages, dtype=np.int32)[None], np.array([n - 1])
+    o = paged.attention_decode(_t(q), K.to(DEV), V.to(DEV), _t(table, torch.int32), _t(pos, torch.int32), scale=1.0, **kw)
+    ref = P.attention_f64(q, kr, vr, table, pos, [0], 1.0)[0, 0, 1]
+    # score 17.5 or 18 (8.75 becomes 9 in e4m3): off by one unit of 2^-23 of it and the exponential's 2^-22 each,
+    # sums of equal terms by 2^-23 a step, the output by half an fp16 step (it is above the subnormals)
+    assert 2e-4 < ref < 2e-3
+    assert abs(float(o[0, 1]) - ref) <= ref * (18 * 2.0 ** -22 + 2.0 ** -21 + n / 8 * 2.0 ** -23 + 2.0 ** -11)
+
+
+def test_attention_without_seq_pads_rows_behind_the_table():
+    args, kw, out, _ = _attention(3, 4, 2, 64, 8, [20, 9, 33], False, 14)
+    q, k, v, table, pos = args
+    more = torch.cat([q, q])
+    o = paged.attention_decode(more, k, v, table, torch.cat([pos, pos]))
+    assert torch.equal(o[:3], out) and torch.all(o[3:] == 0)
+    kk, vv = k.clone(), v.clone()
+    qkv = torch.randn(6, 8 * 64, device=DEV).half()
+    res = torch.full((6, 4, 64), 3.0, dtype=torch.float16, device=DEV)
+    cs = paged.rope_table(40, DEV, rot=32)
+    paged.qknorm_rope_append(qkv, torch.cat([pos, pos]), None, None, cs, kk, vv, table, 4, out=res)
+    assert torch.all(res[3:] == 3.0)
+    k2, v2 = k.clone(), v.clone()
+    paged.qknorm_rope_append(qkv[:3], pos, None, None, cs, k2, v2, table, 4)
+    assert torch.equal(_nan0(kk), _nan0(k2)) and torch.equal(_nan0(vv), _nan0(v2))
+
+
+def _nan0(t):
+    return t.view(torch.int16)
+
+
+def test_attention_infinities_and_nan_where_they_count():
+    """A NaN or infinite value that a row does see reaches its output; other rows and heads stay clean."""
+    k = torch.randn(4, 2, 8, 64, device=DEV).half()
+    v = torch.randn(4, 2, 8, 64, device=DEV).half()
+    q = torch.randn(2, 4, 64, device=DEV).half()
+    table, pos = _t([[0, 1], [2, 3]], torch.int32), _t([15, 15], torch.int32)
+    base = paged.attention_decode(q, k, v, table, pos)
+    k[1, 1, 3, 5], v[2, 0, 0, 7] = float("nan"), float("inf")
+    o = paged.attention_decode(q, k, v, table, pos)
+    a, b = o.view(2, 4, 64), base.view(2, 4, 64)
+    assert torch.all(torch.isnan(a[0, 2:])) and torch.equal(a[0, :2], b[0, :2])
+    assert torch.all(torch.isinf(a[1, :2, 7])) and torch.equal(a[1, 2:], b[1, 2:])
+    keep = [c for c in range(64) if c != 7]
+    assert torch.equal(a[1, :2][:, keep], b[1, :2][:, keep])
+
+
 def test_attention_agrees_with_the_contiguous_caches():
     rng = np.random.default_rng(8)
     M, H, Hkv, Lmax = 3, 16, 2, 320
