@@ -68,9 +68,15 @@ def _row_stride(t, rows, width, name) -> int:
 
 
 def _int32(t, n, name) -> int:
-    if t.dtype != _I32 or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype != _I32 or t.numel() != n or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor with one element per row")
     return t.data_ptr()
+
+
+def _gains(g, dh) -> int:
+    if g.dtype != _FP16 or g.numel() != dh or not g.is_contiguous():
+        raise ValueError("gains must be contiguous float16 [head dim]")
+    return g.data_ptr()
 
 
 def _scale(s, heads) -> int:
@@ -85,10 +91,13 @@ def _cache(k, v, table, k_scale, v_scale):
     if len(shape) != 4 or v.shape != shape or v.stride() != st or v.dtype != dtype:
         raise ValueError("k and v must be alike: [pages][kv heads][page size][head dim]")
     pages, heads, size, dh = shape
-    if st[3] != 1 or st[2] != dh or (st[1] != size * dh and heads > 1):
+    s0, s1, s2, s3 = st
+    if s3 != 1 or s2 != dh or (s1 != size * dh and heads > 1):
         raise ValueError("the heads of a page must be contiguous")
-    tsh, tst = table.shape, table.stride()
-    if table.dtype != _I32 or len(tsh) != 2 or tst[1] != 1:
+    if table.dtype != _I32 or table.dim() != 2:
+        raise ValueError("the page table must be int32 [sequences][pages] with contiguous rows")
+    (seqs, width), (t0, t1) = table.shape, table.stride()
+    if t1 != 1 and width > 1:
         raise ValueError("the page table must be int32 [sequences][pages] with contiguous rows")
     if dtype == _FP16:
         if k_scale is not None or v_scale is not None:
@@ -99,8 +108,8 @@ def _cache(k, v, table, k_scale, v_scale):
     else:
         raise ValueError("a cache is float16 or float8_e4m3fn")
     return _pack(k.data_ptr(), v.data_ptr(), ks, vs, table.data_ptr(), pages, size,
-                 st[0] if pages > 1 else heads * size * dh, heads, dh, tsh[0], tsh[1],
-                 tst[0] if tsh[0] > 1 else tsh[1], code), heads, dh
+                 s0 if pages > 1 else heads * size * dh, heads, dh, seqs, width, t0 if seqs > 1 else width,
+                 code), heads, dh
 
 
 # ---------------------------------------------------------------- operators
@@ -140,13 +149,13 @@ def qknorm_rope_append(qkv: torch.Tensor, pos: torch.Tensor, gq, gk, cs: torch.T
     cache, heads, dh = _cache(k, v, table, k_scale, v_scale)
     if qkv.dim() != 2:
         raise ValueError("qkv must be [rows][(H + 2 Hkv) * head dim]")
-    T = qkv.shape[0]
+    T = len(qkv)
     stride = _row_stride(qkv, T, (H + 2 * heads) * dh, "qkv")
-    if cs.dtype != _F32 or cs.dim() != 3 or cs.shape[2] != 2 or not cs.is_contiguous():
+    angles = cs.shape
+    if cs.dtype != _F32 or len(angles) != 3 or angles[2] != 2 or not cs.is_contiguous():
         raise ValueError("cs must be a contiguous float32 table [positions][rot / 2][2]")
-    for g in (gq, gk):
-        if g is not None and (g.dtype != _FP16 or g.shape != (dh,) or not g.is_contiguous()):
-            raise ValueError("gains must be contiguous float16 [head dim]")
+    gq_p = None if gq is None else _gains(gq, dh)
+    gk_p = None if gk is None else _gains(gk, dh)
     q = out if out is not None else torch.empty(T, H, dh, dtype=_FP16, device=qkv.device)
     q_stride = _row_stride(q, T, H * dh, "out")
     pos_p, seq_p = _int32(pos, T, "pos"), None if seq is None else _int32(seq, T, "seq")
@@ -154,9 +163,8 @@ def qknorm_rope_append(qkv: torch.Tensor, pos: torch.Tensor, gq, gk, cs: torch.T
         return q
     with _on(index):
         st = _lib.lib().tri_paged_qknorm_rope(
-            qkv.data_ptr(), stride, pos_p, seq_p, None if gq is None else gq.data_ptr(),
-            None if gk is None else gk.data_ptr(), cs.data_ptr(), cs.shape[0], 2 * cs.shape[1], 1 if interleaved else 0,
-            q.data_ptr(), q_stride, cache, T, H, eps, _raw_stream(index))
+            qkv.data_ptr(), stride, pos_p, seq_p, gq_p, gk_p, cs.data_ptr(), angles[0], 2 * angles[1],
+            1 if interleaved else 0, q.data_ptr(), q_stride, cache, T, H, eps, _raw_stream(index))
     if st:
         _lib.check(st, "tri_paged_qknorm_rope")
     return q
@@ -176,9 +184,10 @@ def attention_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: t
     in captured graphs never share one."""
     index = _device(q, k, v, table, pos, seq, k_scale, v_scale, out)
     cache, heads, dh = _cache(k, v, table, k_scale, v_scale)
-    if q.dim() != 3 or q.shape[2] != dh:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != dh:
         raise ValueError("q must be [rows][heads][head dim]")
-    M, H, _ = q.shape
+    M, H, _ = shape
     stride = _row_stride(q, M, H * dh, "q")
     y = out if out is not None else torch.empty(M, H * dh, dtype=_FP16, device=q.device)
     out_stride = _row_stride(y, M, H * dh, "out")
