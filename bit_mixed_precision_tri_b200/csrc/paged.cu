@@ -241,6 +241,8 @@ template <int DH, bool FP8, bool INTER>
 __global__ void __launch_bounds__(256)
 paged_append_kernel(const AppendParams p) {
   constexpr int LPH = DH / 8, GROUPS = 256 / LPH;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();                                          // what follows may be the last kernel's
   const int64_t t = blockIdx.x;
   const int j = (int)blockIdx.y * GROUPS + threadIdx.x / LPH;
   const bool exists = j < p.H + 2 * p.Hkv;
@@ -309,6 +311,8 @@ paged_append_stream_kernel(const AppendParams p) {
     fence_mbar_init();
   }
   __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
   const int nh = p.H + 2 * p.Hkv;
   uint32_t polls = kWaitPolls;
   int st = 0;
@@ -425,6 +429,8 @@ copy_pages_kernel(uint8_t* __restrict__ pools, int64_t n_pools, int64_t pool_str
                   const int* __restrict__ dst, int64_t n, int64_t units_per_page) {
   const int lane = threadIdx.x & 31;
   const int64_t units = n * n_pools * units_per_page;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
   for (int64_t u = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); u < units; u += warps) {
     const int64_t c = u % units_per_page, pl = (u / units_per_page) % n_pools, i = u / units_per_page / n_pools;
@@ -441,6 +447,23 @@ copy_pages_kernel(uint8_t* __restrict__ pools, int64_t n_pools, int64_t pool_str
     for (int k = 0; k < 4; ++k)
       if (at + 512 * k < page_bytes) __stcs(reinterpret_cast<uint4*>(to + 512 * k), v[k]);
   }
+}
+
+// programmatic launch: the kernel may start while the one before it ends, and
+// waits for its end before it touches memory
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
@@ -501,8 +524,8 @@ cudaError_t launch_paged_qknorm_rope(const __half* qkv, int64_t qkv_stride, cons
   if (T * ceil_div(nh, groups) <= kFewCtasPerSm * (int64_t)sms) {
     const dim3 grid((unsigned)T, (unsigned)ceil_div(nh, groups));
     return pick([&](auto dh, auto e, auto il) -> cudaError_t {
-      paged_append_kernel<decltype(dh)::value, decltype(e)::value, decltype(il)::value><<<grid, 256, 0, s>>>(p);
-      return cudaGetLastError();
+      return launch_chained(paged_append_kernel<decltype(dh)::value, decltype(e)::value, decltype(il)::value>, grid,
+                            256, 0, s, p);
     });
   }
   const int64_t row_bytes = nh * head_bytes + rot * 4;
@@ -530,8 +553,7 @@ cudaError_t launch_paged_qknorm_rope(const __half* qkv, int64_t qkv_stride, cons
       if (r != cudaSuccess) return r;
       if (dev < 64) ready[dev] = true;
     }
-    kernel<<<(unsigned)ctas, kAppendThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kernel, dim3((unsigned)ctas), kAppendThreads, (size_t)smem, s, p);
   });
 }
 
@@ -542,9 +564,8 @@ cudaError_t launch_copy_pages(uint8_t* pools, int64_t n_pools, int64_t pool_stri
   const int64_t ctas = ceil_div(n * n_pools, 8) < (int64_t(1) << 40) / upp ? ceil_div(n * n_pools * upp, 8)
                                                                              : (int64_t(1) << 40);
   const int64_t most = (int64_t)sms * 64;
-  copy_pages_kernel<<<(unsigned)(ctas < most ? ctas : most), 256, 0, s>>>(
-      pools, n_pools, pool_stride, (int)pages, page_stride, page_bytes, src, dst, n, upp);
-  return cudaGetLastError();
+  return launch_chained(copy_pages_kernel, dim3((unsigned)(ctas < most ? ctas : most)), 256, 0, s, pools, n_pools,
+                        pool_stride, (int)pages, page_stride, page_bytes, src, dst, n, upp);
 }
 
 }  // namespace tri
