@@ -237,6 +237,7 @@ __device__ __forceinline__ void store_value(const AppendParams& p, const Turner<
 }
 
 // Few rows: one head per group, spread over the CTAs, every load issued at once.
+// Latency: 2.0 us a call for one row of 80 heads (the kernel below: 3.9), in a graph.
 template <int DH, bool FP8, bool INTER>
 __global__ void __launch_bounds__(256)
 paged_append_kernel(const AppendParams p) {
@@ -273,8 +274,13 @@ paged_append_kernel(const AppendParams p) {
 // a run of one row's heads where a row is long; up to 25 KB.  The producer warp
 // looks the rows up an item ahead (a lane per row) and bulk-copies them and
 // their angles into a ring of stages, so that every load's latency is behind
-// the items before it; eight warps turn and store.
-constexpr int kFewCtasPerSm = 4;
+// the items before it; eight warps turn and store.  Bound by memory: 16384 rows of 80
+// heads of 128 in fp16 117 us (5.8 TB/s, 89 % of a copy's rate; 122 without the
+// arithmetic), 5001 rows of 96 heads of 64 23-25 us (5.0-5.4 TB/s).
+// CTAs per SM of the few-row kernel up to which it is taken.  Few / many rows' kernel: 4 per SM (118 rows
+// of 80 heads) 3.0 / 5.1 us, 8 (592 of 20) 4.1 / 5.0, 16 (1184 of 20) 6.4 / 6.2, 20 (590 of 80) 7.4 / 8.2,
+// 32 (2400 of 20) 11.0 / 9.4, 40 (1180 of 80) 12.9 / 12.6
+constexpr int kFewCtasPerSm = 14;
 constexpr int kItemBytes = 25 * 1024 + 512;
 constexpr int kAppendStages = 2;
 constexpr int kAppendThreads = 288;
@@ -421,7 +427,10 @@ paged_append_stream_kernel(const AppendParams p) {
 }
 
 // ---------------------------------------------------------------- page copies
-constexpr int kCopyUnit = 2048;                                 // bytes a warp moves at once: 4 x 16 per lane
+// bytes a warp moves at once: 4 x 16 per lane.  1500 pages of 128 KB in 4 pools: 240 us,
+// 6.6 TB/s read and written, the rate of a copy (1 KB a warp: 268 us, 4 KB: 257, when 8
+// CTAs per SM walked the pages; they do so 64 at a time now)
+constexpr int kCopyUnit = 2048;
 
 __global__ void __launch_bounds__(256)
 copy_pages_kernel(uint8_t* __restrict__ pools, int64_t n_pools, int64_t pool_stride, int pages,

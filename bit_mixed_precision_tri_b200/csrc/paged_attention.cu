@@ -21,8 +21,14 @@
 //    to 8 query heads the columns, so that no row is wasted on heads that do not
 //    exist), with the running maximum and sum in fp32 per warp.  O^T += V^T P^T:
 //    V^T comes from ldmatrix.trans, P^T from the S^T accumulators by movmatrix,
-//    in two fp16 parts, so that the fp32 accumulation bounds the error.  e4m3 elements become fp16 (exactly) in
-//    registers; the K scale joins the softmax scale, the V scale the output.
+//    in two fp16 parts, so that the fp32 accumulation bounds the error.  e4m3
+//    elements become fp16 (exactly) in registers; the K scale joins the softmax
+//    scale, the V scale the output.
+//
+// Measured (B200, 64 query heads on 8 of 128 unless said): 16 rows x 4096 positions
+// in fp16 45.9 us (5.8 TB/s of K and V, 89 % of a copy's rate), 1 x 131072 87 us (94 %),
+// 100 ragged rows to 6000 in e4m3 98 us (91 %), 9 ragged rows to 20000 with 16 heads on
+// one 17.7 us (22 %: five tiles a CTA), 1 x 37 5.0 us, all in one graph.
 #include <cuda.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>

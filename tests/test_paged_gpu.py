@@ -155,8 +155,10 @@ def _check_append(T, H, Hkv, dh, ps, rot, inter, norm, fp8, seed, S=None, wide=0
     (37, 5, 1, 64, 8, 64, True, 4),
     (130, 12, 12, 128, 16, 96, False, 7),
     (700, 4, 2, 64, 32, 32, True, 5),
-    (1201, 1, 1, 64, 8, 16, False, 40),      # 32 rows an item, the last one ragged
-    (640, 3, 3, 128, 16, 80, True, 9),
+    (1201, 1, 1, 64, 8, 16, False, 40),
+    (2505, 1, 1, 64, 8, 16, False, 90),      # the many-row kernel: 32 rows an item, the last one ragged
+    (2100, 3, 3, 128, 16, 80, True, 30),
+    (2200, 4, 2, 64, 32, 32, True, 12),
     (301, 90, 10, 128, 64, 128, False, 3),   # a row longer than an item: two runs of heads
     (333, 60, 60, 64, 32, 64, True, 2),
 ])
@@ -164,7 +166,7 @@ def test_append(T, H, Hkv, dh, ps, rot, inter, S, norm, fp8):
     _check_append(T, H, Hkv, dh, ps, rot, inter, norm, fp8, T + H + rot, S)
 
 
-@pytest.mark.parametrize("T", [6, 600])
+@pytest.mark.parametrize("T", [6, 600, 2200])
 def test_append_padding_rows_absent_pages_and_strided_rows(T):
     bad = [("pad", 0), ("far", 1), ("seq", 2), ("negseq", 3), ("hole", 4), ("big", T - 1)]
     w = _check_append(T, 4, 2, 128, 8, 64, False, True, False, 5, S=T, wide=24, break_rows=bad)
