@@ -42,7 +42,11 @@ namespace {
 using namespace ptx;
 
 constexpr int kMaxStages = 8;
-constexpr int kSoloRun = 2;                  // a run of more tiles gives one-tile (row, head)s to single warps
+// A run of more tiles than this gives one-tile (row, head)s to single warps, which
+// take its blocks one after another and need no merge.  With / without, 8 heads x 60
+// positions in fp16: 300 rows (8 tiles a run) 18.5 / 22.4 us, 111 (3) 9.1 / 9.9, 74 (2)
+// 7.6 / 8.0, 16 (1) 6.4 / 5.8, 1 row 5.7 / 5.0.
+constexpr int kSoloRun = 1;
 // Weights are held times 2^14, sums and outputs with them: the two fp16 parts then
 // reach down to 2^-38 of the largest weight instead of 2^-24, below which a hundred
 // thousand small weights would vanish from the output but not from their sum.
