@@ -363,10 +363,12 @@ TRI_API tri_status tri_attention_decode(const uint16_t* q, const uint16_t* kcach
  *   k_scale, v_scale  e4m3 only: float32 [heads], the value of a stored
  *              element is element * scale[head]; scales positive.
  *   table      int32 [seqs][seq_pages], rows table_stride >= 0 elements
- *              apart (0: one row for all): table[s][i] is the page that holds positions i * page_size ..
- *              of sequence s.  An entry outside [0, pages) is an absent page.
+ *              apart (0: one row for all): table[s][i] is the page that holds
+ *              positions i * page_size .. of sequence s.  An entry outside
+ *              [0, pages) is an absent page.
  *              One page may stand in several rows (a shared prefix).
- *   head_dim 64 or 128; page_size a power of two, 8..256; pages <= 2^31 - 1.
+ *   head_dim 64 or 128; page_size a power of two, 8..256; pages <= 2^31 - 1;
+ *   heads <= 65535; seq_pages * page_size <= 2^30.  The pools do not overlap.
  *
  * Rows: a call takes a batch of rows (new tokens).  Row t is position pos[t]
  * of sequence seq[t] (device int32; seq NULL means row t is sequence t).  A
@@ -418,7 +420,8 @@ TRI_API tri_status tri_attention_decode(const uint16_t* q, const uint16_t* kcach
  *   page that stands twice in dst, or in both lists (unless src[i] = dst[i]),
  *   ends up with unspecified bytes; other pages are not touched.  n = 0 does
  *   nothing.
- * Strides are multiples of 8 elements; qkv, q, q_out, out, cs and the gains are
+ * T < 2^31, M <= 2^24, H <= 65535 (append), M * H < 2^31 (attention).
+ * Row strides are multiples of 8 elements; qkv, q, q_out, out, cs and the gains are
  * 16-byte aligned, pos, seq, table, src, dst and the scales 4-byte.  fp16
  * results are rounded once from fp32.  Errors as above, TRI_ERR_INVALID_ARG
  * also for a bad dtype, kind, scale or one gain without the other; nothing
