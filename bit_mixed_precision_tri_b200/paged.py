@@ -16,7 +16,6 @@ on the host, which pages are free and how many sequences share each.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -27,7 +26,6 @@ from .api import Workspace
 RMS_EPS = 1e-5
 ROPE_THETA = 5.0e5
 E4M3 = torch.float8_e4m3fn
-_NULL = contextlib.nullcontext()
 
 
 # A decode step makes these calls for every block and token, so the checks are
@@ -35,13 +33,21 @@ _NULL = contextlib.nullcontext()
 # struct rather than a ctypes one.
 _pack = _lib.PAGED_CACHE.pack
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current = torch.cuda.current_device
 _FP16, _I32, _F32 = torch.float16, torch.int32, torch.float32
 _WS_BYTES = {}
 
 
-def _on(index: int):
-    """The device as the current one (the library launches on the current device)."""
-    return _NULL if torch.cuda.current_device() == index else torch.cuda.device(index)
+def _call(fn, index: int, *args) -> None:
+    """fn(*args, stream) on the device's current stream, the device made the
+    current one if it is not (the library launches on the current device)."""
+    if _current() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _lib.check(st, fn.__name__)
 
 
 def _device(first, *ts) -> int:
@@ -131,9 +137,7 @@ def rope_table(Lmax: int, device, rot: int = 128, theta: float = ROPE_THETA, sca
     sc = None
     if scaling is not None:
         sc = ctypes.byref(_lib.RopeScaling(_lib.ROPE_KINDS[scaling], factor, context, low, high))
-    with _on(index):
-        _lib.check(_lib.lib().tri_rope_table_scaled(cs.data_ptr(), Lmax, rot, float(theta), sc, _raw_stream(index)),
-                   "tri_rope_table_scaled")
+    _call(_lib.lib().tri_rope_table_scaled, index, cs.data_ptr(), Lmax, rot, float(theta), sc)
     return cs
 
 
@@ -161,12 +165,8 @@ def qknorm_rope_append(qkv: torch.Tensor, pos: torch.Tensor, gq, gk, cs: torch.T
     pos_p, seq_p = _int32(pos, T, "pos"), None if seq is None else _int32(seq, T, "seq")
     if T == 0:
         return q
-    with _on(index):
-        st = _lib.lib().tri_paged_qknorm_rope(
-            qkv.data_ptr(), stride, pos_p, seq_p, gq_p, gk_p, cs.data_ptr(), angles[0], 2 * angles[1],
-            1 if interleaved else 0, q.data_ptr(), q_stride, cache, T, H, eps, _raw_stream(index))
-    if st:
-        _lib.check(st, "tri_paged_qknorm_rope")
+    _call(_lib.lib().tri_paged_qknorm_rope, index, qkv.data_ptr(), stride, pos_p, seq_p, gq_p, gk_p, cs.data_ptr(),
+          angles[0], 2 * angles[1], 1 if interleaved else 0, q.data_ptr(), q_stride, cache, T, H, eps)
     return q
 
 
@@ -195,21 +195,18 @@ def attention_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: t
     if M == 0:
         return y
     L = _lib.lib()
-    with _on(index):
-        key = (M, H, heads, dh, index)
-        nbytes = _WS_BYTES.get(key)
-        if nbytes is None:
-            if len(_WS_BYTES) > 4096:
-                _WS_BYTES.clear()
+    key = (M, H, heads, dh, index)
+    nbytes = _WS_BYTES.get(key)
+    if nbytes is None:
+        if len(_WS_BYTES) > 4096:
+            _WS_BYTES.clear()
+        with torch.cuda.device(index):
             nbytes = _WS_BYTES[key] = L.tri_paged_attention_workspace_bytes(M, H, heads, dh) or 256
-        ws = workspace.get(nbytes) if workspace is not None else torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        if ws.get_device() != index:
-            raise ValueError("the workspace must live on the tensors' device")
-        st = L.tri_paged_attention(q.data_ptr(), stride, pos_p, seq_p, cache, y.data_ptr(), out_stride, M, H,
-                                   dh ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
-                                   _raw_stream(index))
-    if st:
-        _lib.check(st, "tri_paged_attention")
+    ws = workspace.get(nbytes) if workspace is not None else torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    if ws.get_device() != index:
+        raise ValueError("the workspace must live on the tensors' device")
+    _call(L.tri_paged_attention, index, q.data_ptr(), stride, pos_p, seq_p, cache, y.data_ptr(), out_stride, M, H,
+          dh ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
     return y
 
 
@@ -257,12 +254,8 @@ def copy_pages(pools: torch.Tensor, src, dst) -> None:
         return
     e = pools.element_size()
     page_bytes = heads * size * dh * e
-    with _on(index):
-        st = _lib.lib().tri_copy_pages(pools.data_ptr(), n_pools, pool_stride * e, pages,
-                                       strides[-4] * e if pages > 1 else page_bytes, page_bytes, src_p, dst_p, n,
-                                       _raw_stream(index))
-    if st:
-        _lib.check(st, "tri_copy_pages")
+    _call(_lib.lib().tri_copy_pages, index, pools.data_ptr(), n_pools, pool_stride * e, pages,
+          strides[-4] * e if pages > 1 else page_bytes, page_bytes, src_p, dst_p, n)
 
 
 # ---------------------------------------------------------------- the cache

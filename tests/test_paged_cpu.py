@@ -293,3 +293,33 @@ def test_wrappers_refuse_host_tensors():
         paged.rope_table(4, "cpu")
     with pytest.raises(ValueError):
         paged.rope_table(4, "cuda", scaling="none")
+
+
+def test_calls_make_the_tensors_device_current(monkeypatch):
+    """A call for tensors of a device that is not the current one switches to it and takes its stream."""
+    entered, got = [], []
+
+    class Device:
+        def __init__(self, index):
+            entered.append(index)
+
+        def __enter__(self):
+            return self
+
+        def __exit__(self, *exc):
+            return False
+
+    def entry(*args):
+        got.append(args)
+        return 0 if args[0] else 2
+
+    monkeypatch.setattr(paged.torch.cuda, "device", Device)
+    monkeypatch.setattr(paged, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(paged, "_current", lambda: 1)
+    paged._call(entry, 0, 7)
+    assert entered == [0] and got == [(7, 100)]
+    paged._call(entry, 1, 8)
+    assert entered == [0] and got[1] == (8, 101)
+    with pytest.raises(_lib.TriError) as e:
+        paged._call(entry, 1, 0)
+    assert e.value.status == 2 and "entry" in str(e.value)
