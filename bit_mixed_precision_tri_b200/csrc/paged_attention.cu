@@ -19,16 +19,18 @@
 //  * Four consumer warps (per 8 query heads) take 16 or 32 positions of a tile each.  Scores are formed
 //    transposed, S^T = K Q^T (mma.sync m16n8k16: positions are the 16 rows, up
 //    to 8 query heads the columns, so that no row is wasted on heads that do not
-//    exist), with the running maximum and sum in fp32 per warp.  O^T += V^T P^T:
+//    exist), with a running reference and sum in fp32 per warp.  O^T += V^T P^T:
 //    V^T comes from ldmatrix.trans, P^T from the S^T accumulators by movmatrix,
 //    in two fp16 parts, so that the fp32 accumulation bounds the error.  e4m3
 //    elements become fp16 (exactly) in registers; the K scale joins the softmax
 //    scale, the V scale the output.
 //
 // Measured (B200, 64 query heads on 8 of 128 unless said): 16 rows x 4096 positions
-// in fp16 45.9 us (5.8 TB/s of K and V, 89 % of a copy's rate), 1 x 131072 87 us (94 %),
-// 100 ragged rows to 6000 in e4m3 98 us (91 %), 9 ragged rows to 20000 with 16 heads on
-// one 17.7 us (22 %: five tiles a CTA), 1 x 37 5.0 us, all in one graph.
+// in fp16 45.2 us (5.9 TB/s of K and V, 91 % of a copy's rate), 1 x 131072 87 us (94 %),
+// 100 ragged rows to 6000 in e4m3 96 us (93 %), 9 ragged rows to 20000 with 16 heads on
+// one 17.1 us (22 %: five tiles a CTA), 1 x 37 4.9 us, all in one graph.  A reference
+// that is raised only when it must be, instead of the exact maximum of every tile, took
+// 9 x 80000 with 16 heads on one in e4m3 from 58.6 to 53.2 us.
 #include <cuda.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
@@ -51,6 +53,8 @@ constexpr int kSoloRun = 1;
 // reach down to 2^-38 of the largest weight instead of 2^-24, below which a hundred
 // thousand small weights would vanish from the output but not from their sum.
 constexpr float kWeightShift = 14.f;
+constexpr float kWeightMost = 15.9f;         // log2 of the largest weight held in fp16 (65504)
+constexpr float kNothing = -1e30f;           // the reference before any position: below every score
 constexpr uint32_t kWaitPolls = 1u << 18;    // about a second
 constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
 
@@ -408,7 +412,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         qf[kk][0] = real ? lds32(a) : 0u;
         qf[kk][1] = real ? lds32(a + (FP8 ? 4 : 16)) : 0u;
       }
-      mx[0] = mx[1] = -INFINITY;
+      mx[0] = mx[1] = kNothing;
       l[0] = l[1] = 0.f;
 #pragma unroll
       for (int fb = 0; fb < DH / 16; ++fb) o[fb][0] = o[fb][1] = o[fb][2] = o[fb][3] = 0.f;
@@ -484,49 +488,53 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         fence_proxy_async();                                       // before TMA refills the stage
         __syncwarp();
       }
-      // ---- running softmax; the eight lanes of a column hold the positions of a set
+      // ---- running softmax.  A column's reference is a maximum of tiles before; it is
+      // raised (the eight lanes of the column agree on the new one, sums and outputs
+      // are scaled) only where a weight would leave fp16, rarely after the first tiles
       uint32_t ph[kSets][2], pl[kSets][2];
-      bool grew = false;
-      float alpha[2];
       float pr[kSets][4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = fmaxf(sc[0][e], sc[0][2 + e]);
-#pragma unroll
-        for (int u = 1; u < kSets; ++u) top = fmaxf(top, fmaxf(sc[u][e], sc[u][2 + e]));
-        top *= c2;
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        const float mnew = fmaxf(mx[e], top);
-        const float top_seen = mnew == -INFINITY ? 0.f : mnew;   // nothing seen yet: all weights 0
-        const float base = top_seen - kWeightShift;
-        alpha[e] = ex2(mx[e] - top_seen);
-        grew |= mnew > mx[e];
-        mx[e] = mnew;
-        float sum = 0.f;
-#pragma unroll
-        for (int u = 0; u < kSets; ++u) {
-          pr[u][e] = ex2(fmaf(sc[u][e], c2, -base));
-          pr[u][2 + e] = ex2(fmaf(sc[u][2 + e], c2, -base));
-          sum += pr[u][e] + pr[u][2 + e];
-        }
-        l[e] = fmaf(l[e], alpha[e], sum);
-      }
+      bool over = false;
 #pragma unroll
       for (int u = 0; u < kSets; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          pr[u][k] = fmaf(sc[u][k], c2, kWeightShift - mx[k & 1]);
+          over |= pr[u][k] > kWeightMost;
+        }
+      if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(sc[0][e], sc[0][2 + e]);
+#pragma unroll
+          for (int u = 1; u < kSets; ++u) top = fmaxf(top, fmaxf(sc[u][e], sc[u][2 + e]));
+          top *= c2;
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+          top = fmaxf(mx[e], fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16)));
+          const float alpha = ex2(mx[e] - top);
+          mx[e] = top;
+          l[e] *= alpha;
+#pragma unroll
+          for (int fb = 0; fb < DH / 16; ++fb) o[fb][e] *= alpha, o[fb][2 + e] *= alpha;
+#pragma unroll
+          for (int u = 0; u < kSets; ++u) {
+            pr[u][e] = fmaf(sc[u][e], c2, kWeightShift - top);
+            pr[u][2 + e] = fmaf(sc[u][2 + e], c2, kWeightShift - top);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kSets; ++u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pr[u][k] = ex2(pr[u][k]);
+        l[0] += pr[u][0] + pr[u][2];
+        l[1] += pr[u][1] + pr[u][3];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           uint32_t hi, lo;
           split_weights(pr[u][2 * r], pr[u][2 * r + 1], hi, lo);
           pl[u][r] = transpose8x8(lo);
           ph[u][r] = transpose8x8(hi);
-        }
-      if (__any_sync(0xFFFFFFFFu, grew)) {                         // rare after the first tiles
-#pragma unroll
-        for (int fb = 0; fb < DH / 16; ++fb) {
-          o[fb][0] *= alpha[0], o[fb][1] *= alpha[1];
-          o[fb][2] *= alpha[0], o[fb][3] *= alpha[1];
         }
       }
       // ---- O^T += V^T P^T
@@ -591,7 +599,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = wml[4 * group + k][2 * tig + e];
       mtop[e] = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
-      const float base = mtop[e] == -INFINITY ? 0.f : mtop[e];
+      const float base = mtop[e];
       lsum[e] = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) lsum[e] = fmaf(w[k].y, ex2(w[k].x - base), lsum[e]);
