@@ -63,7 +63,11 @@ template <int DH, bool FP8, int HG>
 struct Cfg {
   static constexpr int kWarps = 4 * HG;                       // consumer warps
   static constexpr int kThreads = 32 * (kWarps + 2);          // and two producer warps, of K and of V
-  static constexpr int kCtasPerSm = HG == 2 ? 1 : 2;          // eight consumer warps per SM
+  // Two CTAs per SM; one where 320 threads of 164 registers leave no other choice, three
+  // where a position is 64 bytes and registers and stages fit.  (16 heads on one of 64,
+  // 9 x 80000: two CTAs at 96 registers 36.3 us, one at 142 39.8, in fp16; 35.1 and 41.3
+  // in e4m3.  12 heads of 64, 37 x 6000 in e4m3: three CTAs 63.7 us, two 70.3.)
+  static constexpr int kCtasPerSm = HG == 2 && DH == 128 ? 1 : HG == 1 && DH == 64 && FP8 ? 3 : 2;
   static constexpr int kRow = DH * (FP8 ? 1 : 2);             // bytes of a position
   // A warp's chain of dependent steps per tile (scores, maximum, weights, output)
   // takes about 0.7 us whatever its width, so rows of at most 128 bytes come 128 to
@@ -78,7 +82,7 @@ struct Cfg {
   static constexpr int kQRow = DH * 2 + 16;                   // padded: fragment reads hit distinct banks
   static constexpr int kQ = 8 * HG * kQRow;
   static constexpr int kMerge = HG * 2 * DH * 8 * 4;          // two warps' outputs of each group
-  static constexpr int kRoom = (kCtasPerSm == 1 ? 224 : 113) * 1024 - kMerge - 2560;
+  static constexpr int kRoom = (kCtasPerSm == 1 ? 224 : kCtasPerSm == 2 ? 113 : 75) * 1024 - kMerge - 2304;
   static constexpr int kFit = kRoom / (2 * kKV + kQ);
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kSmem = 1024 + kStages * (2 * kKV + kQ) + kMerge;
@@ -781,7 +785,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_p() {
   return fn;
 }
 
-constexpr int kMaxCtasPerSm = 2;
+constexpr int kMaxCtasPerSm = 3;
 // parts per (row, head), as CTAs over (row, head)s, up to which the small join is used: at 4.6 it took
 // 11.8 us against 12.0 (8 rows x 1000 x 8 heads, both kernels), at 2.3 45.9 against 47.9 (16 x 4096), at
 // 7.4 17.4 against 16.6 (5 x 4000), at 37 17.0 against 10.7 (1 x 4096)
