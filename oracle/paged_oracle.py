@@ -156,3 +156,42 @@ def attention_bound(q, K, V, table, pos, seq, scale: float, ref) -> np.ndarray:
             vmax = float(np.max(np.abs(np.asarray(V[at, j, slot], np.float64))))
             tol[m, h] = (2 * (dh + 4) * 2.0 ** -23 * absmax + 2.0 ** -20 + (len(kept) / 8 + 32) * 2.0 ** -23) * vmax
     return tol + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
+
+
+def attention_rows_f64(q, K, V, table, pos, seq, scale: float):
+    """(out, tolerance), both [M][H][dh]: ``attention_f64`` with the heads of a
+    (row, key/value head) in one product, for batches of many positions, and a
+    bound that goes by the weighted values instead of the largest one.
+
+    A weight is off, relative to the others, by rel = 2 (dh + 4) 2^-23 of the
+    scores' absolute sums (see ``attention_bound``) + 2^-20 (exponential, split
+    into two fp16 parts) + (n / 8 + 32) 2^-23 (sums over n positions), and by
+    2^-39 of the largest weight at least (half a step of the smaller part).  So
+    the output is off by rel (sum w |V| / sum w + |out|) + n 2^-39 max |V|, then
+    rounded by half an fp16 step."""
+    q = np.asarray(q, np.float64)
+    M, H, dh = q.shape
+    pages, Hkv, ps, _ = K.shape
+    G = H // Hkv
+    out, tol = np.zeros((M, H, dh)), np.full((M, H, dh), 2.0 ** -25)
+    for m in range(M):
+        n = min(int(pos[m]) + 1, table.shape[1] * ps) if 0 <= int(seq[m]) < table.shape[0] else 0
+        if n <= 0:
+            continue
+        p = np.arange(n)
+        pg = np.asarray(table[int(seq[m])])[p // ps].astype(np.int64)
+        keep = (pg >= 0) & (pg < pages)
+        if not keep.any():
+            continue
+        at, slot, n = pg[keep], p[keep] % ps, int(keep.sum())
+        for j in range(Hkv):
+            k, v, qj = np.asarray(K[at, j, slot], np.float64), np.asarray(V[at, j, slot], np.float64), q[m, j * G:(j + 1) * G]
+            s = qj @ k.T * scale
+            w = np.exp(s - s.max(1, keepdims=True))
+            w /= w.sum(1, keepdims=True)
+            o = w @ v
+            absmax = (np.abs(qj) @ np.abs(k).T).max(1, keepdims=True) * scale
+            rel = 2 * (dh + 4) * 2.0 ** -23 * absmax + 2.0 ** -20 + (n / 8 + 32) * 2.0 ** -23
+            out[m, j * G:(j + 1) * G] = o
+            tol[m, j * G:(j + 1) * G] += rel * (w @ np.abs(v) + np.abs(o)) + n * 2.0 ** -39 * np.abs(v).max() + 2.0 ** -11 * np.abs(o)
+    return out, tol

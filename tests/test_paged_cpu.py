@@ -323,3 +323,15 @@ def test_calls_make_the_tensors_device_current(monkeypatch):
     with pytest.raises(_lib.TriError) as e:
         paged._call(entry, 1, 0)
     assert e.value.status == 2 and "entry" in str(e.value)
+
+
+def test_attention_rows_is_attention():
+    """The oracle for many positions agrees with the plain one, holes, padding and strangers included."""
+    rng = np.random.default_rng(2)
+    q, K, V = rng.standard_normal((6, 6, 64)), rng.standard_normal((9, 2, 8, 64)), rng.standard_normal((9, 2, 8, 64))
+    table = np.array([[0, 1, 2, 8], [3, -1, 5, 9], [-1, -1, 11, -1]])
+    pos, seq = [23, 29, 30, 100, -1, 5], [0, 1, 2, 0, 0, 3]
+    a = P.attention_f64(q, K, V, table, pos, seq, 0.125)
+    b, tol = P.attention_rows_f64(q, K, V, table, pos, seq, 0.125)
+    assert np.allclose(a, b, rtol=1e-12, atol=1e-14) and np.all(tol >= 2.0 ** -25) and not b[2].any() and not b[4:].any()
+    assert np.all(tol <= P.attention_bound(q, K, V, table, pos, seq, 0.125, a) * 2 + 2.0 ** -24)
