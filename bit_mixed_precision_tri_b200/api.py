@@ -291,6 +291,13 @@ def selftest_wait_timeout(which: int, device=None) -> None:
         _lib.check(st, "tri_selftest_wait_timeout")
 
 
+def selftest_wait_polls(polls: int = -1) -> None:
+    """How often the waits of the paged kernels poll before they give up, for
+    launches from now on (-1: the default).  With 0 each gives up at once: what a
+    call leaves behind then can be checked (``wait_status``: 51-53, 61-63)."""
+    _lib.check(_lib.lib().tri_selftest_wait_polls(int(polls)), "tri_selftest_wait_polls")
+
+
 class TernaryLinear:
     """A ternary linear layer: absmean-ternarized, packed weights and a GEMM.
 

@@ -284,7 +284,6 @@ constexpr int kFewCtasPerSm = 14;
 constexpr int kItemBytes = 25 * 1024 + 512;
 constexpr int kAppendStages = 2;
 constexpr int kAppendThreads = 288;
-constexpr uint32_t kWaitPolls = 1u << 18;                       // about a second
 constexpr unsigned kAppendProducerCode = 61, kAppendConsumerCode = 62, kAppendDrainCode = 63;
 
 // the items of a CTA: block (of rows) and chunk (of heads), gridDim.x apart

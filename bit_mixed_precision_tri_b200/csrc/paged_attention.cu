@@ -55,7 +55,6 @@ constexpr int kSoloRun = 1;
 constexpr float kWeightShift = 14.f;
 constexpr float kWeightMost = 15.9f;         // log2 of the largest weight held in fp16 (65504)
 constexpr float kNothing = -1e30f;           // the reference before any position: below every score
-constexpr uint32_t kWaitPolls = 1u << 18;    // about a second
 constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
 
 // HG: groups of 8 query heads per key/value head, 1 or 2
@@ -109,6 +108,7 @@ struct Params {
   unsigned* error;
   int64_t q_stride, out_stride, table_stride, M;
   int heads, G, page_shift, pages, seqs, max_len, ctas;
+  unsigned polls;             // of a wait for a stage
   float scale;
 };
 
@@ -211,8 +211,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   __shared__ uint64_t full[C::kStages], empty[C::kStages];
   __shared__ Desc desc[C::kStages];
   __shared__ __align__(16) float2 wml[kWarps][8];
-  __shared__ long long sums[kWarps + 2], s_first_prefix;
+  __shared__ long long sums[kWarps + 2], s_first_offset;
   __shared__ int s_first_row;
+  __shared__ volatile int s_gave_up;                             // a consumer's wait ran out
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto row_tiles = [](int len) { return (len + kTile - 1) >> kTileShift; };
 
@@ -220,8 +221,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 2);
       mbar_init(&empty[s], kWarps);
-      desc[s] = Desc{};                                          // in range whatever becomes of a wait
     }
+    s_gave_up = 0;
     fence_mbar_init();
   }
   if (warp >= kWarps && lane == 0) prefetch_tensormap(warp == kWarps ? &kmap : &vmap);
@@ -262,7 +263,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       at += t;
     }
     s_first_row = (int)m;
-    s_first_prefix = at;
+    s_first_offset = w0 - at * p.heads;
   }
   __syncthreads();
   // rows with nothing to read take no tiles: their zeros are dealt out by row
@@ -291,7 +292,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int box_x = part * (C::kBox / (FP8 ? 1 : 2));
     int64_t m = s_first_row;
     int s, L = row_length(p, m, s), T = row_tiles(L);
-    const int64_t off = w0 - (int64_t)s_first_prefix * p.heads;
+    const int64_t off = s_first_offset;
     int h = (int)(off / T), t = (int)(off % T);
     // the next row's length, read a row ahead
     int s_next = -1, L_next = m + 1 < p.M ? row_length(p, m + 1, s_next) : 0;
@@ -303,10 +304,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     };
     int id = lookup(s, L, t);
     int4 split_rec = make_int4(0, 0, 0, 0);
-    uint32_t polls = kWaitPolls;
     int st = 0;
     uint32_t phase = 1;                                         // of `empty`; nothing to wait for in the first round
-    for (int64_t i = 0; i < ntiles; ++i, ++st) {
+    int64_t i = 0;
+    for (; i < ntiles; ++i, ++st) {
       if (st == C::kStages) st = 0, phase ^= 1;
       const int cm = (int)m, ch = h, ct = t, cT = T, cL = L, cid = id;
       // step on, and look the next tile's page up while this stage's slot frees
@@ -322,9 +323,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
       }
       if (i + 1 < ntiles) id = lookup(s, L, t);
-      if (i >= C::kStages && !mbar_wait(&empty[st], phase, polls)) {
+      // a wait that runs out ends the loads: a stage that is not free is not armed again
+      if (i >= C::kStages && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase, p.polls))) {
         if (lane == 0) record_wait_failure(p.error, kProducerCode);
-        polls = 1;
+        break;
       }
       const bool first = i == 0 || ct == 0, last = i + 1 == ntiles || ct == cT - 1;
       const unsigned loaded = __ballot_sync(0xFFFFFFFFu, cid >= 0);
@@ -367,8 +369,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     if (lane == 0 && !is_v && !by_seg) p.recs[blockIdx.x] = split_rec;
     // every copy has landed before the CTA may leave
-    for (int64_t i = ntiles > C::kStages ? ntiles - C::kStages : 0; i < ntiles; ++i)
-      if (!mbar_wait(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1, kWaitPolls) && lane == 0)
+    for (int64_t j = i > C::kStages ? i - C::kStages : 0; j < i; ++j)
+      if (!mbar_wait(&full[j % C::kStages], (uint32_t)(j / C::kStages) & 1, kWaitPolls) && lane == 0)
         record_wait_failure(p.error, kDrainCode);
     return;
   }
@@ -387,15 +389,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   float o[DH / 16][4];
   float mx[2], l[2];
   float c2 = 0.f;
-  uint32_t polls = kWaitPolls, phase = 0;
+  uint32_t phase = 0;
   int st = 0;
-  for (int64_t i = 0; i < ntiles; ++i, ++st) {
+  int64_t i = 0;
+  for (; i < ntiles; ++i, ++st) {
     if (st == C::kStages) st = 0, phase ^= 1;
-    if (!mbar_wait(&full[st], phase, polls)) {
-      if (lane == 0) record_wait_failure(p.error, kConsumerCode);
-      polls = 1;
-    }
-    __syncwarp();
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], phase, p.polls))) break;
     const Desc d = desc[st];
     // a one-tile (row, head) in a longer run is one warp's, with no merge; its
     // neighbours are the other warps'
@@ -628,6 +627,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       put(buf + quarter * kVec);
     }
     named_bar_sync(1 + group, 128);
+    if (s_gave_up) continue;                                     // a warp of the four had nothing to add
     // every warp adds and stores a quarter of the features
     const bool open = d.flags & (kOpenLeft | kOpenRight);
     const int64_t slot = 2 * (int64_t)blockIdx.x + ((d.flags & kOpenLeft) ? 0 : 1);
@@ -641,6 +641,32 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       const float4 y = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
       if (open) p.part[slot * HG * kVec + (fb * HG + group) * 32 + lane] = y;
       else store_out<DH, FP8>(dst, h0, p.G, 16 * fb, gid, y, i0, i1);
+    }
+  }
+  if (i == ntiles) return;
+  // ---- the wait for tile i ran out.  What the stage says may be an older tile's, and the
+  // other warps of the group may still get theirs: this one reads and stores nothing
+  // more, but passes the barriers of the merges it has left, which it counts from the
+  // rows' lengths as the producers do, so that no barrier waits for it
+  if (lane == 0) {
+    record_wait_failure(p.error, kConsumerCode);
+    s_gave_up = 1;
+  }
+  __syncwarp();
+  int64_t m = s_first_row;
+  int s, T = row_tiles(row_length(p, m, s)), h = (int)(s_first_offset / T);
+  for (int64_t at = -(s_first_offset % T);;) {                   // tiles at .. at + T - 1 of the run: a (row, head)
+    const int64_t end = at + T;
+    if ((end < ntiles ? end : ntiles) > i && !(T == 1 && ntiles > kSoloRun))
+      for (int b = 0; b < 3; ++b) named_bar_sync(1 + group, 128);
+    if (end >= ntiles) return;
+    at = end;
+    if (++h == p.heads) {
+      h = 0;
+      do {                                                       // the next row that has anything
+        if (++m == p.M) return;
+        T = row_tiles(row_length(p, m, s));
+      } while (T == 0);
     }
   }
 }
@@ -878,7 +904,7 @@ cudaError_t launch_paged_attention(const __half* q, int64_t q_stride, const int*
   p.q = q, p.pos = pos, p.seq = seq, p.table = c.table, p.k_scale = c.k_scale, p.v_scale = c.v_scale, p.out = out;
   p.q_stride = q_stride, p.out_stride = out_stride, p.table_stride = c.table_stride, p.M = M;
   p.heads = (int)c.heads, p.G = (int)(H / c.heads), p.pages = (int)c.pages, p.seqs = (int)c.seqs;
-  p.max_len = (int)(c.seq_pages * c.page_size), p.scale = scale;
+  p.max_len = (int)(c.seq_pages * c.page_size), p.scale = scale, p.polls = wait_polls();
   while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
   const bool fp8 = c.dtype == TRI_CACHE_E4M3, wide = p.G > 8;
   if (c.head_dim == 128) {

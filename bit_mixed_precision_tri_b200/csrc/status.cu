@@ -7,6 +7,7 @@
 // unspecified, but nothing traps and the context stays usable.  The word is
 // per device (one copy per loaded module), looked up once per device with
 // that device current; the host reads and clears it with tri_wait_status.
+#include <atomic>
 #include <mutex>
 
 #include "sm100_ptx.cuh"
@@ -17,6 +18,8 @@ namespace tri {
 static __device__ unsigned g_wait_status;
 
 namespace {
+
+std::atomic<unsigned> g_polls{kWaitPolls};
 
 constexpr int kMaxDev = 64;
 unsigned* g_word[kMaxDev];
@@ -45,6 +48,9 @@ __global__ void expire_wait_kernel(unsigned* word, const unsigned long long* nev
 }
 
 }  // namespace
+
+unsigned wait_polls() { return g_polls.load(std::memory_order_relaxed); }
+void set_wait_polls(unsigned polls) { g_polls.store(polls, std::memory_order_relaxed); }
 
 cudaError_t wait_status_word(unsigned** out) {
   int dev = -1;

@@ -409,6 +409,12 @@ tri_status tri_selftest_wait_timeout(int which, void* scratch, void* stream) {
   return from_cuda(tri::launch_expire_wait(which, scratch, static_cast<cudaStream_t>(stream)));
 }
 
+tri_status tri_selftest_wait_polls(int64_t polls) {
+  if (polls < -1 || polls > (int64_t)tri::kWaitPolls) return TRI_ERR_INVALID_ARG;
+  tri::set_wait_polls(polls < 0 ? tri::kWaitPolls : (unsigned)polls);
+  return TRI_OK;
+}
+
 tri_status tri_gemm_tq2(const uint16_t* X, const uint8_t* qs, const uint16_t* d, uint16_t* Y,
                         int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
                         void* stream) {

@@ -111,6 +111,12 @@ cudaError_t launch_gemm_tc(int fmt, const __half* X, const uint8_t* qs, const __
 // 51-53 paged_attention.cu, 61-63 paged.cu
 constexpr unsigned kSelfTestMbarCode = 90;
 constexpr unsigned kSelfTestStampCode = 91;
+// polls after which a wait of the paged kernels gives up (about a second; a drain of
+// copies in flight always takes that many), and the limit of launches from now on:
+// kWaitPolls, or less where a test has set it
+constexpr unsigned kWaitPolls = 1u << 18;
+unsigned wait_polls();
+void set_wait_polls(unsigned polls);
 // the current device's status word (device address)
 cudaError_t wait_status_word(unsigned** out);
 // synchronizes `s`, then copies the word to *code and optionally zeroes it

@@ -283,9 +283,14 @@ TRI_API tri_status tri_gemm_swiglu(int format, int path, const uint16_t* X, cons
  *   first 8 bytes of `scratch`, device memory, 8-byte aligned, zeroed by the
  *   call).  The wait runs out within about a second, records its code and
  *   returns; nothing faults.  It lets a caller check the detection path.
+ * tri_selftest_wait_polls: how often a wait of the paged kernels polls before it
+ *   gives up, 0 .. 2^18, for launches of this process from then on; -1 restores
+ *   the default, 2^18.  With 0 every wait gives up at once, so that a caller can
+ *   check what such a call leaves behind.  Needs no device.
  * ---------------------------------------------------------------------- */
 TRI_API tri_status tri_wait_status(uint32_t* code, int clear, void* stream);
 TRI_API tri_status tri_selftest_wait_timeout(int which, void* scratch, void* stream);
+TRI_API tri_status tri_selftest_wait_polls(int64_t polls);
 
 /* Kernel that tri_gemm would launch for this call under TRI_PATH_AUTO
  * (one of tri_gemm_path), or -1 if the shape is invalid. */

@@ -335,3 +335,10 @@ def test_attention_rows_is_attention():
     b, tol = P.attention_rows_f64(q, K, V, table, pos, seq, 0.125)
     assert np.allclose(a, b, rtol=1e-12, atol=1e-14) and np.all(tol >= 2.0 ** -25) and not b[2].any() and not b[4:].any()
     assert np.all(tol <= P.attention_bound(q, K, V, table, pos, seq, 0.125, a) * 2 + 2.0 ** -24)
+
+
+def test_selftest_wait_polls_refusals(L):
+    for bad in (-2, (1 << 18) + 1, 1 << 40):
+        assert L.tri_selftest_wait_polls(bad) == 1
+    for good in (0, 1 << 18, -1):
+        assert L.tri_selftest_wait_polls(good) == 0
