@@ -400,6 +400,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // neighbours are the other warps'
     const bool solo = d.flags & kSolo;
     if (solo && (int)(i & 3) != quarter) {
+      __syncwarp();                                              // every lane has read desc[st]
       if (lane == 0) mbar_arrive(&empty[st]);
       continue;
     }
