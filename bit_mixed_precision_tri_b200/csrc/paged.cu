@@ -347,6 +347,7 @@ paged_append_stream_kernel(const AppendParams p) {
       const int h0 = item.chunk * p.heads, nhc = nh - h0 < p.heads ? nh - h0 : p.heads;
       place[st][lane] = make_int2(pp, page);
       const int live = __popc(__ballot_sync(0xFFFFFFFFu, pp >= 0));
+      __syncwarp();                                             // a vote orders no memory: the places, then the arrival
       if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(live * (nhc * DH * 2 + p.rot * 4)));
       __syncwarp();
       if (pp >= 0) {
