@@ -63,6 +63,7 @@ struct AppendParams {
   int64_t qkv_stride, q_stride, table_stride, page_stride, T, cs_rows;
   int H, Hkv, rot, pages, seqs, page_shift, max_pos;
   float eps;
+  unsigned polls;                               // of a wait for a stage
   // of the many-row kernel: rows and heads of an item, chunks of heads per row,
   // blocks of rows, steps of gridDim.x items, log2 of the groups of lanes per row
   int rows, heads, chunks, next_chunk, gpt_shift, stage_bytes;
@@ -319,7 +320,6 @@ paged_append_stream_kernel(const AppendParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int nh = p.H + 2 * p.Hkv;
-  uint32_t polls = kWaitPolls;
   int st = 0;
   if (warp == 8) {
     uint32_t phase = 1;
@@ -340,9 +340,10 @@ paged_append_stream_kernel(const AppendParams p) {
       const int page_next = pp_next >= 0 ? row_page(p, pp_next, sq_next) : -1;
       int sq2 = 0;
       const int pp2 = look(item2, sq2);
-      if (n >= kAppendStages && !mbar_wait(&empty[st], phase, polls)) {
+      // a wait that runs out ends the loads: a stage that is not free is not armed again
+      if (n >= kAppendStages && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase, p.polls))) {
         if (lane == 0) record_wait_failure(p.error, kAppendProducerCode);
-        polls = 1;
+        break;
       }
       const int h0 = item.chunk * p.heads, nhc = nh - h0 < p.heads ? nh - h0 : p.heads;
       place[st][lane] = make_int2(pp, page);
@@ -371,12 +372,10 @@ paged_append_stream_kernel(const AppendParams p) {
   uint32_t phase = 0;
   for (Item item(p); item.block < p.blocks; item.next(p), ++st) {
     if (st == kAppendStages) st = 0, phase ^= 1;
-    const bool arrived = mbar_wait(&full[st], phase, polls);
-    if (!arrived) {                                             // nothing of the item is stored
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], phase, p.polls))) {
       if (lane == 0) record_wait_failure(p.error, kAppendConsumerCode);
-      polls = 1;
+      return;                                                   // this warp stores nothing more, and frees no stage
     }
-    __syncwarp();
     const int64_t t0 = item.block * p.rows;
     const int h0 = item.chunk * p.heads, nhc = nh - h0 < p.heads ? nh - h0 : p.heads;
     // of the item's heads, h0 .. h0 + nhc - 1: queries, keys, values
@@ -386,7 +385,7 @@ paged_append_stream_kernel(const AppendParams p) {
     const int gk = nq + ((gi - nq) & (gpt - 1)), gv = nqk + ((gi - nqk) & (gpt - 1));
     const uint8_t* stage = sm + st * p.stage_bytes;
     for (int r0 = 0; r0 < p.rows; r0 += per_pass) {             // shuffles below: trip counts are the CTA's
-      const bool real = arrived && r0 + gr < p.rows;
+      const bool real = r0 + gr < p.rows;
       const int r = r0 + gr < p.rows ? r0 + gr : p.rows - 1;
       const int2 at = place[st][r];
       const bool valid = real && at.x >= 0;
@@ -515,7 +514,7 @@ cudaError_t launch_paged_qknorm_rope(const __half* qkv, int64_t qkv_stride, cons
   p.qkv_stride = qkv_stride, p.q_stride = q_stride, p.table_stride = c.table_stride;
   p.page_stride = c.page_stride, p.T = T, p.cs_rows = cs_rows;
   p.H = (int)H, p.Hkv = (int)c.heads, p.rot = (int)rot, p.pages = (int)c.pages;
-  p.seqs = (int)c.seqs, p.max_pos = (int)(c.seq_pages * c.page_size), p.eps = eps;
+  p.seqs = (int)c.seqs, p.max_pos = (int)(c.seq_pages * c.page_size), p.eps = eps, p.polls = wait_polls();
   while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
   const int groups = (int)(256 * 8 / c.head_dim);
   const int64_t nh = H + 2 * c.heads, head_bytes = c.head_dim * 2;

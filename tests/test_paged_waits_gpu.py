@@ -67,3 +67,36 @@ def test_attention_of_one_tile_rows_whose_waits_run_out_stores_nothing(polls):
         assert torch.all(out == 3.0)
         polls(-1)
         assert not torch.any(paged.attention_decode(q, k, v, table, pos, out=out) == 3.0) and tri.wait_status(DEV) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("limit", [0, 1])
+def test_append_whose_waits_run_out_returns(polls, limit, fp8):
+    """3000 rows of 6 heads take the kernel that streams them; with no poll at all it stores nothing."""
+    T, H, Hkv, dh, ps = 3000, 4, 1, 128, 64
+    g = torch.Generator().manual_seed(5)
+    qkv = torch.randn(T, (H + 2 * Hkv) * dh, generator=g).half().to(DEV)
+    pages = -(-T // ps)
+    table, pos = torch.arange(pages, dtype=torch.int32, device=DEV)[None], torch.arange(T, dtype=torch.int32, device=DEV)
+    seq, cs = torch.zeros_like(pos), paged.rope_table(pages * ps, DEV)
+    one = torch.full((Hkv,), 0.05, device=DEV)
+    kw = dict(k_scale=one, v_scale=one) if fp8 else {}
+
+    def call():
+        k, v = (torch.full((pages, Hkv, ps, dh), 3.0, device=DEV).to(torch.float8_e4m3fn if fp8 else torch.float16)
+                for _ in range(2))
+        q = torch.full((T, H, dh), 3.0, dtype=torch.float16, device=DEV)
+        paged.qknorm_rope_append(qkv, pos, None, None, cs, k, v, table, H, seq=seq, out=q, **kw)
+        code = tri.wait_status(DEV, clear=True)
+        return code, q, k.view(torch.uint8), v.view(torch.uint8)
+
+    code, *want = call()
+    assert code == 0
+    polls(limit)
+    code, *got = call()
+    polls(-1)
+    assert code in ((61, 62) if limit == 0 else (0, 61, 62, 63))
+    if limit == 0:
+        assert torch.all(got[0] == 3.0) and len(set(got[1].flatten().tolist())) <= 2 and torch.equal(got[1], got[2])
+    code, *again = call()
+    assert code == 0 and all(torch.equal(a, b) for a, b in zip(again, want))
