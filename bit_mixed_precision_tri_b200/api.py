@@ -293,8 +293,9 @@ def selftest_wait_timeout(which: int, device=None) -> None:
 
 def selftest_wait_polls(polls: int = -1) -> None:
     """How often the waits of the paged kernels poll before they give up, for
-    launches from now on (-1: the default).  With 0 each gives up at once: what a
-    call leaves behind then can be checked (``wait_status``: 51-53, 61-63)."""
+    launches from now on (-1: the default).  With 0 nothing is loaded and every
+    wait runs out: what a call leaves behind then can be checked (``wait_status``:
+    51-53, 61-63)."""
     _lib.check(_lib.lib().tri_selftest_wait_polls(int(polls)), "tri_selftest_wait_polls")
 
 

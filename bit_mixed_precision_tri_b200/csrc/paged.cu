@@ -335,13 +335,13 @@ paged_append_stream_kernel(const AppendParams p) {
     item2.next(p);
     int pp_next = look(item2, sq_next);
     item2.next(p);
-    for (; item.block < p.blocks; item.next(p), item2.next(p), ++n, ++st) {
+    for (; item.block < p.blocks && p.polls != 0; item.next(p), item2.next(p), ++n, ++st) {   // 0: a test's, nothing is loaded
       if (st == kAppendStages) st = 0, phase ^= 1;
       const int page_next = pp_next >= 0 ? row_page(p, pp_next, sq_next) : -1;
       int sq2 = 0;
       const int pp2 = look(item2, sq2);
       // a wait that runs out ends the loads: a stage that is not free is not armed again
-      if (n >= kAppendStages && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase, p.polls))) {
+      if (n >= kAppendStages && !__all_sync(0xFFFFFFFFu, mbar_wait_after_poll(&empty[st], phase, p.polls))) {
         if (lane == 0) record_wait_failure(p.error, kAppendProducerCode);
         break;
       }
@@ -372,7 +372,7 @@ paged_append_stream_kernel(const AppendParams p) {
   uint32_t phase = 0;
   for (Item item(p); item.block < p.blocks; item.next(p), ++st) {
     if (st == kAppendStages) st = 0, phase ^= 1;
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], phase, p.polls))) {
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait_after_poll(&full[st], phase, p.polls))) {
       if (lane == 0) record_wait_failure(p.error, kAppendConsumerCode);
       return;                                                   // this warp stores nothing more, and frees no stage
     }

@@ -213,7 +213,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   __shared__ __align__(16) float2 wml[kWarps][8];
   __shared__ long long sums[kWarps + 2], s_first_offset;
   __shared__ int s_first_row;
-  __shared__ volatile int s_gave_up;                             // a consumer's wait ran out
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto row_tiles = [](int len) { return (len + kTile - 1) >> kTileShift; };
 
@@ -222,7 +221,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       mbar_init(&full[s], 2);
       mbar_init(&empty[s], kWarps);
     }
-    s_gave_up = 0;
     fence_mbar_init();
   }
   if (warp >= kWarps && lane == 0) prefetch_tensormap(warp == kWarps ? &kmap : &vmap);
@@ -307,7 +305,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     int st = 0;
     uint32_t phase = 1;                                         // of `empty`; nothing to wait for in the first round
     int64_t i = 0;
-    for (; i < ntiles; ++i, ++st) {
+    for (; i < ntiles && p.polls != 0; ++i, ++st) {             // 0: a test's, nothing is loaded
       if (st == C::kStages) st = 0, phase ^= 1;
       const int cm = (int)m, ch = h, ct = t, cT = T, cL = L, cid = id;
       // step on, and look the next tile's page up while this stage's slot frees
@@ -324,7 +322,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       }
       if (i + 1 < ntiles) id = lookup(s, L, t);
       // a wait that runs out ends the loads: a stage that is not free is not armed again
-      if (i >= C::kStages && !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase, p.polls))) {
+      if (i >= C::kStages && !__all_sync(0xFFFFFFFFu, mbar_wait_after_poll(&empty[st], phase, p.polls))) {
         if (lane == 0) record_wait_failure(p.error, kProducerCode);
         break;
       }
@@ -394,7 +392,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   int64_t i = 0;
   for (; i < ntiles; ++i, ++st) {
     if (st == C::kStages) st = 0, phase ^= 1;
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], phase, p.polls))) break;
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait_after_poll(&full[st], phase, p.polls))) break;
     const Desc d = desc[st];
     // a one-tile (row, head) in a longer run is one warp's, with no merge; its
     // neighbours are the other warps'
@@ -628,7 +626,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       put(buf + quarter * kVec);
     }
     named_bar_sync(1 + group, 128);
-    if (s_gave_up) continue;                                     // a warp of the four had nothing to add
     // every warp adds and stores a quarter of the features
     const bool open = d.flags & (kOpenLeft | kOpenRight);
     const int64_t slot = 2 * (int64_t)blockIdx.x + ((d.flags & kOpenLeft) ? 0 : 1);
@@ -648,18 +645,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   // ---- the wait for tile i ran out.  What the stage says may be an older tile's, and the
   // other warps of the group may still get theirs: this one reads and stores nothing
   // more, but passes the barriers of the merges it has left, which it counts from the
-  // rows' lengths as the producers do, so that no barrier waits for it
-  if (lane == 0) {
-    record_wait_failure(p.error, kConsumerCode);
-    s_gave_up = 1;
-  }
-  __syncwarp();
+  // rows' lengths as the producers do, so that no barrier waits for it.  Its part of their
+  // sums is NaN, and so is what they make of it
+  if (lane == 0) record_wait_failure(p.error, kConsumerCode);
   int64_t m = s_first_row;
   int s, T = row_tiles(row_length(p, m, s)), h = (int)(s_first_offset / T);
   for (int64_t at = -(s_first_offset % T);;) {                   // tiles at .. at + T - 1 of the run: a (row, head)
     const int64_t end = at + T;
-    if ((end < ntiles ? end : ntiles) > i && !(T == 1 && ntiles > kSoloRun))
+    if ((end < ntiles ? end : ntiles) > i && !(T == 1 && ntiles > kSoloRun)) {
+      if (lane < 8) wml[warp][lane] = make_float2(kNothing, NAN);
       for (int b = 0; b < 3; ++b) named_bar_sync(1 + group, 128);
+    }
     if (end >= ntiles) return;
     at = end;
     if (++h == p.heads) {

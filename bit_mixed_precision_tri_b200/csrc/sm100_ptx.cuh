@@ -52,6 +52,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   return false;
 }
 
+// The same with one poll before the limit is looked at, which mostly succeeds.
+__device__ __forceinline__ bool mbar_wait_after_poll(uint64_t* bar, uint32_t parity, uint32_t limit) {
+  return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, limit);
+}
+
 __device__ __forceinline__ unsigned long long ld_relaxed_u64(const unsigned long long* a) {
   unsigned long long v;
   asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a) : "memory");

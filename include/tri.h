@@ -285,8 +285,8 @@ TRI_API tri_status tri_gemm_swiglu(int format, int path, const uint16_t* X, cons
  *   returns; nothing faults.  It lets a caller check the detection path.
  * tri_selftest_wait_polls: how often a wait of the paged kernels polls before it
  *   gives up, 0 .. 2^18, for launches of this process from then on; -1 restores
- *   the default, 2^18.  With 0 every wait gives up at once, so that a caller can
- *   check what such a call leaves behind.  Needs no device.
+ *   the default, 2^18.  With 0 they load nothing, so that every wait runs out and
+ *   a caller can check what such a call leaves behind.  Needs no device.
  * ---------------------------------------------------------------------- */
 TRI_API tri_status tri_wait_status(uint32_t* code, int clear, void* stream);
 TRI_API tri_status tri_selftest_wait_timeout(int which, void* scratch, void* stream);

@@ -1,6 +1,6 @@
 """Waits of the paged kernels that run out: the call returns, the status word
 names the wait, and the next call is right.  ``selftest_wait_polls`` shortens
-the waits; with 0 polls each gives up at once, with 1 some do and some do not."""
+the waits; with 0 nothing is loaded and each runs out, with 1 some do and some do not."""
 import time
 
 import numpy as np
