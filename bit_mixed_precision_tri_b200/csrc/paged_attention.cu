@@ -50,7 +50,7 @@ constexpr int kMaxStages = 8;
 // 7.6 / 8.0, 16 (1) 6.4 / 5.8, 1 row 5.7 / 5.0.
 constexpr int kSoloRun = 1;
 // Weights are held times 2^14, sums and outputs with them: the two fp16 parts then
-// reach down to 2^-38 of the largest weight instead of 2^-24, below which a hundred
+// reach down to 2^-39 of the largest weight instead of 2^-25, below which a hundred
 // thousand small weights would vanish from the output but not from their sum.
 constexpr float kWeightShift = 14.f;
 constexpr float kWeightMost = 15.9f;         // log2 of the largest weight held in fp16 (65504)
@@ -130,17 +130,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// Two weights as two fp16 parts each, both at least the smallest fp16 (2^-38 of the
-// largest weight, see kWeightShift): with parts of one sign, neither of them 0, an
-// infinite value stays infinite.  The high part is rounded down, the low one is the
-// rest to 2^-21 of the weight.  A NaN stays one.
+// Two weights as two fp16 parts each, the lower the rest to 2^-20.6 of the weight and to
+// 2^-39 of the largest (half a step of fp16's smallest numbers, see kWeightShift).  A
+// weight of 0 is 0 in both.  The high part is taken a little short of the weight
+// (2^-12 of it and 2^-24) so that above 2^-37 of the largest both parts are positive and an
+// infinite value stays infinite: 0 times it would be NaN.  A NaN stays one.
 __device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 least = __halves2half2(__ushort_as_half(1), __ushort_as_half(1));
-  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
-  const __half2 h = __hmax2_nan(*reinterpret_cast<const __half2*>(&hi), least);
-  const float2 f = __half22float2(h);
-  const __half2 g = __hmax2_nan(__floats2half2_rn(a - f.x, b - f.y), least);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
+  float x, y;
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(x), "=f"(y) : "f"(a), "f"(b), "f"(1.f - 1.f / 4096.f), "f"(-1.f / 16777216.f));
+  asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  const __half2 g = __floats2half2_rn(a - f.x, b - f.y);
   lo = *reinterpret_cast<const uint32_t*>(&g);
 }
 // four e4m3 codes as fp16: bytes 0, 1 and bytes 2, 3

@@ -413,6 +413,9 @@ TRI_API tri_status tri_attention_decode(const uint16_t* q, const uint16_t* kcach
  *   page_size of them) whose page is present; key/value head h / (H / heads),
  *   H / heads <= 16.  A row with nothing left, padding included, gives zeros.
  *   What the pages hold behind pos[t] does not matter (Inf and NaN included).
+ *   Weights are held to 2^-39 of the row's largest; one of 0 in float32 counts
+ *   for nothing.  An infinite value gives an infinite output where its weight is
+ *   above 2^-37 of the largest, NaN below.
  *   q and out rows q_stride and out_stride elements apart.  Nothing about the
  *   lengths is needed on the host, so one captured graph serves every length.
  *   workspace: tri_paged_attention_workspace_bytes (0 for shapes it refuses),

@@ -734,3 +734,36 @@ def test_block_refuses_what_its_cache_cannot_serve():
         blk.step(x, pos)
     with pytest.raises(ValueError):
         blk.step(x, pos, 16, seq=pos)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G", [1, 9])
+@pytest.mark.parametrize("gap", [8, 16, 20, 24, 26, 27, 28, 32, 60, 120])
+def test_attention_small_weights_carry_what_they_weigh(gap, G, fp8):
+    """One key outweighs 131071 others by e^gap; its value is small (2^-10) beside theirs
+    (96), so the others are all of the output, half of it, or nothing: where their
+    weight is 0 in float32 the output is the one value."""
+    n, dh, ps = 131072, 64, 256
+    big = gap / 4
+    k = torch.zeros(n // ps, 1, ps, dh)
+    v = torch.full((n // ps, 1, ps, dh), 96.0)
+    k[300, 0, 17, 0], v[300, 0, 17] = big, 2.0 ** -10
+    q = torch.zeros(1, G, dh)
+    q[..., 0] = 4.0
+    kw = dict(k_scale=torch.ones(1, device=DEV), v_scale=torch.full((1,), 2.0 ** -1, device=DEV)) if fp8 else {}
+    dt = E4M3 if fp8 else torch.float16
+    if fp8:
+        v *= 2
+        v[300, 0, 17] = 2.0 ** -9
+    gap = 4 * float(torch.tensor(big).to(dt).float())          # what the cache holds
+    o = paged.attention_decode(q.half().to(DEV), k.to(dt).to(DEV), v.to(dt).to(DEV),
+                               torch.arange(n // ps, dtype=torch.int32, device=DEV)[None], _t([n - 1], torch.int32),
+                               scale=1.0, **kw).float().cpu().numpy().astype(np.float64)
+    w = np.exp(-float(gap))
+    ref = (2.0 ** -10 + (n - 1) * w * 96) / (1 + (n - 1) * w)
+    # the weights' split: 2^-39 of the largest each, half of fp16's smallest step; else as attention_rows_f64
+    rel = 2 * gap * 2.0 ** -22 + 2.0 ** -20 + (n / 8 + 32) * 2.0 ** -23
+    tol = rel * 2 * ref + min(w, 2.0 ** -39) * n * 96 + 2.0 ** -11 * ref + 2.0 ** -25
+    assert np.all(np.abs(o - ref) <= tol), (o[0, 0], ref, tol)
+    if gap >= 104:                                            # e^-104 is 0 in float32
+        assert np.all(o == 2.0 ** -10)
