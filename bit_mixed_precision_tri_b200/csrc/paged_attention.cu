@@ -54,7 +54,7 @@ constexpr int kSoloRun = 1;
 // thousand small weights would vanish from the output but not from their sum.
 constexpr float kWeightShift = 14.f;
 constexpr float kWeightMost = 15.9f;         // log2 of the largest weight held in fp16 (65504)
-constexpr float kNothing = -1e30f;           // the reference before any position: below every score
+constexpr float kNothing = -3e38f;           // the reference before any position: below every score
 constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
 
 // HG: groups of 8 query heads per key/value head, 1 or 2
@@ -129,6 +129,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// log2 of a weight (with the shift) from a score and the column's reference.  The product is
+// rounded by itself, as the reference's was: the score that is the reference gives exactly 0
+// however large it is, where a fused product would leave a rounding error (beyond 2^24:
+// powers of two).  The shift is rounded down, so that none is above kWeightShift by rounding.
+__device__ __forceinline__ float weight_shift(float mx) { return __fadd_rd(kWeightShift, -mx); }
+__device__ __forceinline__ float log2_weight(float score, float c2, float shift) {
+  return __fadd_rn(__fmul_rn(score, c2), shift);
 }
 // Two weights as two fp16 parts each, the lower the rest to 2^-20.6 of the weight and to
 // 2^-39 of the largest (half a step of fp16's smallest numbers, see kWeightShift).  A
@@ -497,12 +505,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       // are scaled) only where a weight would leave fp16, rarely after the first tiles
       uint32_t ph[kSets][2], pl[kSets][2];
       float pr[kSets][4];
+      float down[2] = {weight_shift(mx[0]), weight_shift(mx[1])};
       bool over = false;
 #pragma unroll
       for (int u = 0; u < kSets; ++u)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          pr[u][k] = fmaf(sc[u][k], c2, kWeightShift - mx[k & 1]);
+          pr[u][k] = log2_weight(sc[u][k], c2, down[k & 1]);
           over |= pr[u][k] > kWeightMost;
         }
       if (__any_sync(0xFFFFFFFFu, over)) {
@@ -511,7 +520,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           float top = fmaxf(sc[0][e], sc[0][2 + e]);
 #pragma unroll
           for (int u = 1; u < kSets; ++u) top = fmaxf(top, fmaxf(sc[u][e], sc[u][2 + e]));
-          top *= c2;
+          top = __fmul_rn(top, c2);
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
           top = fmaxf(mx[e], fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16)));
@@ -520,12 +529,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           l[e] *= alpha;
 #pragma unroll
           for (int fb = 0; fb < DH / 16; ++fb) o[fb][e] *= alpha, o[fb][2 + e] *= alpha;
-#pragma unroll
-          for (int u = 0; u < kSets; ++u) {
-            pr[u][e] = fmaf(sc[u][e], c2, kWeightShift - top);
-            pr[u][2 + e] = fmaf(sc[u][2 + e], c2, kWeightShift - top);
-          }
+          down[e] = weight_shift(top);
         }
+#pragma unroll
+        for (int u = 0; u < kSets; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pr[u][k] = log2_weight(sc[u][k], c2, down[k & 1]);
       }
 #pragma unroll
       for (int u = 0; u < kSets; ++u) {

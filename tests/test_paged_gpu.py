@@ -767,3 +767,40 @@ def test_attention_small_weights_carry_what_they_weigh(gap, G, fp8):
     assert np.all(np.abs(o - ref) <= tol), (o[0, 0], ref, tol)
     if gap >= 104:                                            # e^-104 is 0 in float32
         assert np.all(o == 2.0 ** -10)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G", [1, 9])
+@pytest.mark.parametrize("size", [3e3, 1e4, 3e4, 6e4])
+def test_attention_scores_of_any_size(size, G, fp8):
+    """Scores of 10^6 to 10^12.  Equal ones, of either sign, give the mean of the
+    values; different ones are further apart than float32's error of a score, so
+    the largest takes all."""
+    n, dh, ps = 700, 64, 16
+    rng = np.random.default_rng(int(size) + G)
+    ks = torch.tensor([size / 400], device=DEV)
+    kw = dict(k_scale=ks, v_scale=torch.ones(1, device=DEV)) if fp8 else {}
+    dt = E4M3 if fp8 else torch.float16
+    pages = -(-n // ps)
+    table, pos = torch.arange(pages, dtype=torch.int32, device=DEV)[None], _t([n - 1], torch.int32)
+    vals = torch.from_numpy(rng.integers(-8, 9, (pages, 1, ps, dh)).astype(np.float32))
+    V = vals.numpy().astype(np.float64).reshape(-1, dh)[:n]
+    kmax = 400.0 if fp8 else size
+    for sign in (1.0, -1.0):
+        for scale in (None, 1e20):
+            k = torch.full((pages, 1, ps, dh), kmax).to(dt)
+            q = torch.full((1, G, dh), sign * size).half()
+            o = _np(paged.attention_decode(q.to(DEV), k.to(DEV), vals.to(dt).to(DEV), table, pos, scale=scale, **kw))
+            # equal weights: sums of integers below 2^13 with a split to 2^-20, one division, one rounding to fp16
+            ref = V.mean(0)
+            assert np.all(np.abs(o.reshape(G, dh) - ref) <= 2.0 ** -11 * np.abs(ref) + 2.0 ** -19 * np.abs(V).mean(0) + 2.0 ** -24), (sign, scale, o)
+    k = torch.from_numpy((rng.standard_normal((pages, 1, ps, dh)) * kmax / 4).clip(-kmax, kmax).astype(np.float32)).to(dt)
+    q = D.rn16((rng.standard_normal((1, G, dh)) * size / 4).clip(-size, size))
+    K = k.float().numpy().astype(np.float64).reshape(-1, dh)[:n] * (float(ks) if fp8 else 1.0)
+    s = q[0] @ K.T * dh ** -0.5
+    two = np.sort(s, 1)[:, -2:]
+    err = 2 * (dh + 4) * 2.0 ** -23 * (np.abs(q[0]) @ np.abs(K).T).max(1) * dh ** -0.5
+    clear = two[:, 1] - two[:, 0] > err + 110                 # e^-110 is 0 in float32
+    assert clear.any()
+    o = _np(paged.attention_decode(_t(q), k.to(DEV), vals.to(dt).to(DEV), table, pos, **kw)).reshape(G, dh)
+    assert np.all(np.isfinite(o)) and np.array_equal(o[clear], V[s.argmax(1)][clear])
