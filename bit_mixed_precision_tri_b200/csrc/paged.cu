@@ -9,6 +9,7 @@
 //  * copy_pages_kernel: page src[i] of every pool to page dst[i].
 #include <cuda_fp8.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "sm100_ptx.cuh"
@@ -514,7 +515,10 @@ cudaError_t launch_paged_qknorm_rope(const __half* qkv, int64_t qkv_stride, cons
   p.qkv_stride = qkv_stride, p.q_stride = q_stride, p.table_stride = c.table_stride;
   p.page_stride = c.page_stride, p.T = T, p.cs_rows = cs_rows;
   p.H = (int)H, p.Hkv = (int)c.heads, p.rot = (int)rot, p.pages = (int)c.pages;
-  p.seqs = (int)c.seqs, p.max_pos = (int)(c.seq_pages * c.page_size), p.eps = eps, p.polls = wait_polls();
+  p.seqs = (int)c.seqs, p.max_pos = (int)(c.seq_pages * c.page_size), p.polls = wait_polls();
+  // below the normal numbers the root would flush it, and a head of zeros be 0 x Inf; to a mean
+  // that is not 0, 2^-55 at least, neither adds anything
+  p.eps = eps > 0.f && eps < FLT_MIN ? FLT_MIN : eps;
   while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
   const int groups = (int)(256 * 8 / c.head_dim);
   const int64_t nh = H + 2 * c.heads, head_bytes = c.head_dim * 2;

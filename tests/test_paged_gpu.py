@@ -804,3 +804,20 @@ def test_attention_scores_of_any_size(size, G, fp8):
     assert clear.any()
     o = _np(paged.attention_decode(_t(q), k.to(DEV), vals.to(dt).to(DEV), table, pos, **kw)).reshape(G, dh)
     assert np.all(np.isfinite(o)) and np.array_equal(o[clear], V[s.argmax(1)][clear])
+
+
+@pytest.mark.parametrize("T", [2, 2500])
+def test_append_eps_below_the_normal_numbers(T):
+    """x / sqrt(mean x^2 + eps) of a head of zeros is 0 for any eps above 0."""
+    k = torch.ones(-(-T // 8), 1, 8, 64, dtype=torch.float16, device=DEV)
+    v = torch.zeros_like(k)
+    qkv = torch.zeros(T, 192, dtype=torch.float16, device=DEV)
+    qkv[1, :] = 2.0 ** -24                                   # the smallest number: mean x^2 is 2^-48
+    table, pos = torch.arange(len(k), dtype=torch.int32, device=DEV)[None], torch.arange(T, dtype=torch.int32, device=DEV)
+    one = torch.ones(64, dtype=torch.float16, device=DEV)
+    q = paged.qknorm_rope_append(qkv, pos, one, one, paged.rope_table(T, DEV, rot=16), k, v, table, 1,
+                                 seq=torch.zeros_like(pos), eps=1e-40)
+    keep = [t for t in range(T) if t != 1]
+    assert torch.all(q[keep] == 0) and not torch.any(torch.isnan(k))
+    assert torch.all(k.transpose(1, 2).reshape(-1, 64)[:T][keep] == 0)
+    assert torch.all((q[1, 0, 16:] - 1).abs() <= 2.0 ** -11)     # features that do not rotate
