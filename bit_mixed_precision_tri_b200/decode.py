@@ -113,9 +113,10 @@ class DecodeBlock:
     The caches are contiguous, [M][Hkv][Lmax][128], or, with ``cache`` (a
     ``paged.PagedCache`` that the blocks of a model share), pages of its
     ``layer``: the M rows of a step are then any rows of its sequences, negative
-    positions padding.  ``cs`` replaces the rotary table of Lmax positions
-    (``paged.rope_table``: stretched angles, part of the head) and
-    ``interleaved`` its pairing, with ``cache`` only."""
+    positions padding.  ``cs`` replaces the rotary table (``paged.rope_table``:
+    stretched angles, part of the head) and ``interleaved`` its pairing, with
+    ``cache`` only; it must hold every position that a row of the page table has
+    room for, as the default table does whatever Lmax."""
 
     def __init__(self, weights: dict, D: int, H: int, Hkv: int, F: int, M: int, Lmax: int, device,
                  fmt: str = "tq2", eps: float = RMS_EPS, theta: float = ROPE_THETA, cache: "paged.PagedCache" = None,
@@ -126,6 +127,12 @@ class DecodeBlock:
         if cache is not None and (tuple(cache.pools.shape[3:4]) != (Hkv,) or cache.pools.shape[5] != HEAD_DIM or
                                   not 0 <= layer < cache.layers):
             raise ValueError("the cache must have this block's key/value heads, of 128, and its layer")
+        room = 0 if cache is None else cache.table.shape[1] * cache.page_size
+        if cs is not None and (cs.dtype != torch.float32 or cs.dim() != 3 or cs.shape[2] != 2 or
+                               cs.shape[1] not in range(8, HEAD_DIM // 2 + 1, 8) or not cs.is_contiguous()):
+            raise ValueError("cs must be a contiguous float32 table [positions][rot / 2][2], rot a multiple of 16")
+        if cs is not None and cs.shape[0] < room:
+            raise ValueError(f"cs has {cs.shape[0]} positions, a sequence of the cache room for {room}")
         self.cache, self.layer, self.interleaved = cache, layer, interleaved
         self.D, self.H, self.Hkv, self.F, self.M, self.Lmax, self.fmt, self.eps = D, H, Hkv, F, M, Lmax, fmt, eps
         self.dev = dev
@@ -143,7 +150,7 @@ class DecodeBlock:
         if cache is None:
             self.kcache = torch.zeros(M, Hkv, Lmax, HEAD_DIM, dtype=torch.float16, device=dev)
             self.vcache = torch.zeros_like(self.kcache)
-        self.cs = cs if cs is not None else rope_table(Lmax, dev, theta)
+        self.cs = cs if cs is not None else rope_table(max(Lmax, room), dev, theta)
         f16 = dict(dtype=torch.float16, device=dev)
         self.buf = {"xn": torch.empty(M, D, **f16), "qkv": torch.empty(M, (H + 2 * Hkv) * HEAD_DIM, **f16),
                     "q": torch.empty(M, H, HEAD_DIM, **f16), "attn": torch.empty(M, H * HEAD_DIM, **f16),
@@ -162,8 +169,9 @@ class DecodeBlock:
     def step(self, x: torch.Tensor, pos: torch.Tensor, max_len: int = None, path: int = PATH_AUTO,
              seq: torch.Tensor = None) -> torch.Tensor:
         """One decode step: x [M][D] fp16 (the new tokens' residual stream),
-        pos [M] int32 device positions (< Lmax), max_len >= max(pos) + 1 (which
-        a paged cache does not need).  seq [M] int32: the rows' sequences in a
+        pos [M] int32 device positions (< Lmax, or what a sequence of the paged
+        cache has room for), max_len >= max(pos) + 1 (which a paged cache does not
+        need).  seq [M] int32: the rows' sequences in a
         paged cache, which must have room for the positions (without it row m is
         sequence m).  Returns the block output [M][D] (a buffer reused by the
         next step)."""

@@ -342,3 +342,16 @@ def test_selftest_wait_polls_refusals(L):
         assert L.tri_selftest_wait_polls(bad) == 1
     for good in (0, 1 << 18, -1):
         assert L.tri_selftest_wait_polls(good) == 0
+
+
+def test_block_refuses_a_rotary_table_its_cache_outgrows():
+    """A row behind the table would write no key and attend with the last step's queries."""
+    from bit_mixed_precision_tri_b200 import decode as dec
+    cache = paged.PagedCache(6, 2, 3, 4, "cpu", page_size=8)         # 32 positions a sequence
+    good = torch.zeros(32, 32, 2)
+    for bad in (good[:31], torch.zeros(31, 64, 2), good.double(), good[:, :, 0], good[:, :12], torch.zeros(32, 72, 2),
+                torch.zeros(32, 4, 2), torch.zeros(32, 2, 32).transpose(1, 2)):
+        with pytest.raises(ValueError, match="cs "):
+            dec.DecodeBlock({}, 512, 4, 2, 512, 1, 32, "cpu", cache=cache, cs=bad)
+    with pytest.raises(KeyError):                                    # the table is taken; there are no weights
+        dec.DecodeBlock({}, 512, 4, 2, 512, 1, 32, "cpu", cache=cache, cs=good)

@@ -821,3 +821,20 @@ def test_append_eps_below_the_normal_numbers(T):
     assert torch.all(q[keep] == 0) and not torch.any(torch.isnan(k))
     assert torch.all(k.transpose(1, 2).reshape(-1, 64)[:T][keep] == 0)
     assert torch.all((q[1, 0, 16:] - 1).abs() <= 2.0 ** -11)     # features that do not rotate
+
+
+def test_block_on_pages_has_angles_for_every_position_of_its_cache():
+    """A block whose Lmax is below what its cache has room for: the default table covers the cache."""
+    Dm, F, H, Hkv = 512, 512, 4, 2
+    w = _block_weights(Dm, F, H, Hkv, 9)
+    outs = []
+    for Lmax in (16, 64):
+        cache = paged.PagedCache(8, Hkv, 1, 8, DEV, page_size=8)
+        s = cache.new(41)
+        cache.pools.view(torch.int16).copy_(torch.arange(cache.pools.numel(), device=DEV).view(cache.pools.shape) % 15000)
+        blk = dec.DecodeBlock(w, Dm, H, Hkv, F, 1, Lmax, DEV, cache=cache)
+        x = _t(D.rn16(np.random.default_rng(1).standard_normal((1, Dm))))
+        blk.step(x * 0.5, _t([3], torch.int32), seq=_t([s], torch.int32))
+        outs.append(blk.step(x, _t([40], torch.int32), seq=_t([s], torch.int32)).clone())
+        assert blk.cs.shape[0] == 64
+    assert torch.equal(*outs) and torch.all(torch.isfinite(outs[0]))
