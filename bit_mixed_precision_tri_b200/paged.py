@@ -265,8 +265,12 @@ class CacheFull(RuntimeError):
 
 
 class PageBook:
-    """Which pages each sequence holds (host only): pages are shared by
-    counting, and a page that more than one sequence holds is never written.
+    """Which pages each sequence holds (host only): pages are shared by counting.
+
+    Rows are written at positions that ``extend`` made room for after the
+    sequence was last forked, or that ``own`` was called for: no page that more
+    than one sequence holds is written then.  The book cannot see writes, so
+    whoever forks a sequence with positions that are not written yet says so.
 
     Every method that changes what the device must see returns the copies
     (source and destination pages) to be made before the next write."""
@@ -334,6 +338,24 @@ class PageBook:
             if p >= 0:
                 self.count[p] += 1
         return t
+
+    def own(self, s: int, first: int):
+        """Positions of s from `first` to its end are to be written: their pages that
+        another sequence holds too are exchanged for own ones, the first of which
+        is copied where it holds positions below `first`."""
+        if first < 0 or first > self.length[s]:
+            raise ValueError("first must be between 0 and the sequence's length")
+        held = self.pages[s] if first < self.length[s] else []
+        shared = [i for i in range(first // self.page_size, len(held)) if held[i] >= 0 and self.count[held[i]] > 1]
+        if len(shared) > len(self.free_pages):
+            raise CacheFull("no free pages")
+        src, dst = [], []
+        for i in shared:
+            old, held[i] = held[i], self._take()
+            self._drop(old)
+            if i * self.page_size < first:
+                src, dst = [old], [held[i]]
+        return src, dst
 
     def drop_front(self, s: int, n: int) -> None:
         """Give up the pages that hold only positions below n."""
@@ -439,9 +461,21 @@ class PagedCache:
         if src or len(self.book.pages[s]) != before:
             self._sync(s)
 
-    def fork(self, s: int) -> int:
-        """A new sequence that continues s: it shares the pages until one of the two writes."""
+    def fork(self, s: int, written: int = None) -> int:
+        """A new sequence that continues s: the two share s's pages, and ``extend``
+        copies the one that they would both write into.  All positions of s must
+        have been written before the fork; where room was made for more, ``written``
+        says how many are, and the new sequence gets own pages for the others (the
+        page that holds both kinds is copied)."""
         t = self.book.fork(s)
+        if written is not None:
+            try:
+                src, dst = self.book.own(t, written)
+            except (CacheFull, ValueError):
+                self.book.free(t)
+                raise
+            if src:
+                copy_pages(self.pools, src, dst)
         self._sync(t)
         return t
 

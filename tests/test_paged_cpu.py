@@ -355,3 +355,61 @@ def test_block_refuses_a_rotary_table_its_cache_outgrows():
             dec.DecodeBlock({}, 512, 4, 2, 512, 1, 32, "cpu", cache=cache, cs=bad)
     with pytest.raises(KeyError):                                    # the table is taken; there are no weights
         dec.DecodeBlock({}, 512, 4, 2, 512, 1, 32, "cpu", cache=cache, cs=good)
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_cache_forked_between_room_and_write(seed, monkeypatch):
+    """Room is made, sequences are forked, then each writes what it has room for: all
+    read back their own, whoever shares the pages below."""
+    c = paged.PagedCache(30, 1, 6, 9, "cpu", page_size=8, head_dim=64)
+    flat = c.pools[0, 0, :, 0, :, 0]                                 # one number per position of K
+
+    def copy(pools, src, dst):
+        flat[dst] = flat[src]
+    monkeypatch.setattr(paged, "copy_pages", copy)
+    r, ref = random.Random(seed), {}                                # handle -> what it wrote
+    at = lambda s, p: (int(c.table[s, p // 8]), p % 8)
+    mark = 0
+    for _ in range(300):
+        op = r.choice("neewwwffxc")
+        s = r.choice(list(ref)) if ref else None
+        try:
+            if op == "n":
+                ref[c.new(r.randrange(0, 12))] = []
+            elif op == "c":
+                c.compact()
+            elif s is None:
+                continue
+            elif op == "e":
+                c.extend(s, r.randrange(0, 12))
+            elif op == "w":
+                for p in range(len(ref[s]), r.randint(len(ref[s]), c.length(s))):
+                    mark += 1
+                    flat[at(s, p)] = mark % 2000
+                    ref[s].append(mark % 2000)
+            elif op == "f":
+                before = [list(c.book.count), c.length(s), dict(c.book.pages)]
+                t = c.fork(s, written=len(ref[s]))
+                ref[t] = list(ref[s])
+                assert c.length(t) == c.length(s)
+                if c.length(s) == len(ref[s]):
+                    assert c.book.pages[t] == c.book.pages[s]       # all written: all shared
+            else:
+                c.free(s)
+                del ref[s]
+        except paged.CacheFull:
+            if op == "f":
+                assert before == [c.book.count, c.length(s), c.book.pages]
+        for s, vals in ref.items():
+            assert [float(flat[at(s, p)]) for p in range(len(vals))] == vals, (s, op)
+
+
+def test_fork_refuses_more_than_there_is():
+    c = paged.PagedCache(4, 1, 3, 4, "cpu", page_size=8, head_dim=64)
+    s = c.new(9)
+    for bad in (-1, 10):
+        with pytest.raises(ValueError):
+            c.fork(s, written=bad)
+    assert c.free_pages == 2 and len(c.book.free_seqs) == 2 and c.book.count[:2] == [1, 1]
+    t = c.fork(s)
+    assert c.book.pages[t] == c.book.pages[s] and c.free_pages == 2
