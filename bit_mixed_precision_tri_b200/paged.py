@@ -332,8 +332,9 @@ class PageBook:
         """A new sequence that shares every page of s."""
         if not self.free_seqs:
             raise CacheFull("no free row in the page table")
+        held = list(self.pages[s])                          # before the row is taken: s may not exist
         t = self.new()
-        self.pages[t], self.length[t] = list(self.pages[s]), self.length[s]
+        self.pages[t], self.length[t] = held, self.length[s]
         for p in self.pages[t]:
             if p >= 0:
                 self.count[p] += 1
@@ -446,7 +447,7 @@ class PagedCache:
         s = self.book.new()
         try:
             self.book.extend(s, n)
-        except CacheFull:
+        except (CacheFull, ValueError):
             self.book.free(s)
             raise
         self._sync(s)

@@ -413,3 +413,17 @@ def test_fork_refuses_more_than_there_is():
     assert c.free_pages == 2 and len(c.book.free_seqs) == 2 and c.book.count[:2] == [1, 1]
     t = c.fork(s)
     assert c.book.pages[t] == c.book.pages[s] and c.free_pages == 2
+
+
+def test_refused_calls_take_no_row():
+    c = paged.PagedCache(4, 1, 2, 4, "cpu", page_size=8, head_dim=64)
+    s = c.new(3)
+    for _ in range(3):
+        with pytest.raises(ValueError):
+            c.new(-1)
+        with pytest.raises(KeyError):
+            c.fork(s + 1)
+        with pytest.raises(paged.CacheFull):
+            c.new(100)
+    assert len(c.book.free_seqs) == 1 and list(c.book.pages) == [s] and c.free_pages == 3
+    assert c.fork(s) == s + 1
