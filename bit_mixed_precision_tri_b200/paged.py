@@ -405,7 +405,7 @@ class PagedCache:
             raise ValueError("page_size is a power of two from 8 to 256, head_dim 64 or 128")
         if min(num_pages, Hkv, max_seqs, seq_pages, layers) < 1:
             raise ValueError("sizes must be positive")
-        if (dtype == E4M3) != (k_scale is not None and v_scale is not None):
+        if [k_scale is not None, v_scale is not None] != [dtype == E4M3] * 2:
             raise ValueError("an e4m3 cache, and no other, takes k_scale and v_scale")
         self.device = torch.device(device)
         self.layers, self.page_size = layers, page_size

@@ -427,3 +427,10 @@ def test_refused_calls_take_no_row():
             c.new(100)
     assert len(c.book.free_seqs) == 1 and list(c.book.pages) == [s] and c.free_pages == 3
     assert c.fork(s) == s + 1
+
+
+def test_paged_cache_takes_both_scales_or_none():
+    one = torch.ones(2)
+    for kw in (dict(k_scale=one), dict(v_scale=one), dict(dtype=paged.E4M3, k_scale=one), dict(dtype=paged.E4M3, v_scale=one)):
+        with pytest.raises(ValueError, match="takes k_scale and v_scale"):
+            paged.PagedCache(6, 2, 3, 4, "cpu", **kw)
