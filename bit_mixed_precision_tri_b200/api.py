@@ -162,7 +162,7 @@ def _workspace_for(device, stream_handle: int) -> Workspace:
 
 
 class WaitGaveUp(RuntimeError):
-    """A bounded wait inside a GEMM kernel ran out (code in ``.code``); the
+    """A bounded wait inside a GEMM or paged kernel ran out (code in ``.code``); the
     output of the call is unspecified."""
 
     def __init__(self, code: int, what: str):
@@ -268,7 +268,7 @@ def gemm_swiglu(X: torch.Tensor, qs: torch.Tensor, d: torch.Tensor, F: int, K: i
 
 def wait_status(device=None, clear: bool = True) -> int:
     """Synchronize the device's current stream and return its wait status
-    word: 0, or the code of the first bounded wait inside a GEMM kernel that
+    word: 0, or the code of the first bounded wait inside a GEMM or paged kernel that
     gave up since the last clear (that call's output is then unspecified)."""
     dev = torch.device(device or "cuda")
     code = ctypes.c_uint32(0)

@@ -21,7 +21,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .api import Workspace
+from .api import Workspace, _check_waits
 
 RMS_EPS = 1e-5
 ROPE_THETA = 5.0e5
@@ -144,11 +144,15 @@ def rope_table(Lmax: int, device, rot: int = 128, theta: float = ROPE_THETA, sca
 def qknorm_rope_append(qkv: torch.Tensor, pos: torch.Tensor, gq, gk, cs: torch.Tensor, k: torch.Tensor,
                        v: torch.Tensor, table: torch.Tensor, H: int, seq: torch.Tensor = None,
                        interleaved: bool = False, k_scale: torch.Tensor = None, v_scale: torch.Tensor = None,
-                       eps: float = RMS_EPS, out: torch.Tensor = None) -> torch.Tensor:
+                       eps: float = RMS_EPS, out: torch.Tensor = None, check: bool = False) -> torch.Tensor:
     """Queries [T][H][dh] of the fused QKV rows [T][(H + 2 Hkv) dh], normed
     (unless gq and gk are None) and rotated; keys (normed, rotated) and values
     written into the pages of their rows.  ``cs`` is a table of
-    ``rope_table`` ([positions][rot/2][2]); the first rot features rotate."""
+    ``rope_table`` ([positions][rot/2][2]); the first rot features rotate.
+
+    ``check=True`` (for debugging; it synchronizes the stream) reads the device's
+    wait status word after the call and raises WaitGaveUp if a bounded wait
+    inside the kernel ran out."""
     index = _device(qkv, pos, gq, gk, cs, k, v, table, seq, k_scale, v_scale, out)
     cache, heads, dh = _cache(k, v, table, k_scale, v_scale)
     if qkv.dim() != 2:
@@ -167,6 +171,8 @@ def qknorm_rope_append(qkv: torch.Tensor, pos: torch.Tensor, gq, gk, cs: torch.T
         return q
     _call(_lib.lib().tri_paged_qknorm_rope, index, qkv.data_ptr(), stride, pos_p, seq_p, gq_p, gk_p, cs.data_ptr(),
           angles[0], 2 * angles[1], 1 if interleaved else 0, q.data_ptr(), q_stride, cache, T, H, eps)
+    if check:
+        _check_waits(qkv.device, _raw_stream(index), "tri_paged_qknorm_rope")
     return q
 
 
@@ -176,12 +182,13 @@ def attention_workspace_bytes(M: int, H: int, Hkv: int, head_dim: int = 128) -> 
 
 def attention_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, pos: torch.Tensor,
                      seq: torch.Tensor = None, k_scale: torch.Tensor = None, v_scale: torch.Tensor = None,
-                     scale: float = None, out: torch.Tensor = None, workspace: Workspace = None) -> torch.Tensor:
+                     scale: float = None, out: torch.Tensor = None, workspace: Workspace = None,
+                     check: bool = False) -> torch.Tensor:
     """softmax(scale K q) V over positions 0..pos[m] of sequence seq[m] whose
     page is present (zeros where nothing is left); q [M][H][dh] -> [M][H * dh].
     ``scale`` defaults to 1 / sqrt(dh).  Without ``workspace`` each call takes
     its scratch from the caching allocator, so that calls on other streams and
-    in captured graphs never share one."""
+    in captured graphs never share one.  ``check`` as in ``qknorm_rope_append``."""
     index = _device(q, k, v, table, pos, seq, k_scale, v_scale, out)
     cache, heads, dh = _cache(k, v, table, k_scale, v_scale)
     shape = q.shape
@@ -207,6 +214,8 @@ def attention_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: t
         raise ValueError("the workspace must live on the tensors' device")
     _call(L.tri_paged_attention, index, q.data_ptr(), stride, pos_p, seq_p, cache, y.data_ptr(), out_stride, M, H,
           dh ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
+    if check:
+        _check_waits(q.device, _raw_stream(index), "tri_paged_attention")
     return y
 
 

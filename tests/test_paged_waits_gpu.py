@@ -100,3 +100,25 @@ def test_append_whose_waits_run_out_returns(polls, limit, fp8):
         assert torch.all(got[0] == 3.0) and len(set(got[1].flatten().tolist())) <= 2 and torch.equal(got[1], got[2])
     code, *again = call()
     assert code == 0 and all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+def test_check_option(polls):
+    """check=True returns as without it, and raises WaitGaveUp with the wait's code."""
+    args, kw, _ = batch(8, 4, 128, 64, False, 40, 900, 1)
+    want = paged.attention_decode(*args, **kw)
+    assert torch.equal(paged.attention_decode(*args, check=True, **kw), want)
+    polls(0)
+    with pytest.raises(tri.WaitGaveUp) as e:
+        paged.attention_decode(*args, check=True, **kw)
+    assert e.value.code in (51, 52)
+    T = 3000
+    k = torch.zeros(T // 8, 1, 8, 64, dtype=torch.float16, device=DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    rows = (torch.zeros(T, 192, dtype=torch.float16, device=DEV), pos, None, None, paged.rope_table(T, DEV, rot=16), k,
+            k.clone(), torch.arange(T // 8, dtype=torch.int32, device=DEV)[None], 1, torch.zeros_like(pos))
+    with pytest.raises(tri.WaitGaveUp) as e:
+        paged.qknorm_rope_append(*rows, check=True)
+    assert e.value.code in (61, 62)
+    polls(-1)
+    paged.qknorm_rope_append(*rows, check=True)
+    assert torch.equal(paged.attention_decode(*args, check=True, **kw), want)
