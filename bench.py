@@ -96,12 +96,14 @@ def load_peaks():
         return dict(FALLBACK_PEAKS), "fallback"
 
 
-def kernel_source_hash():
+def kernel_source_hash(cs=os.path.join(ROOT, "bit_mixed_precision_tri_b200", "csrc")):
+    """Of the sources that the GEMM kernels' device code comes from (the other
+    header that they include declares host functions)."""
     h = hashlib.sha256()
-    cs = os.path.join(ROOT, "bit_mixed_precision_tri_b200", "csrc")
     for fn in sorted(os.listdir(cs)):
-        with open(os.path.join(cs, fn), "rb") as f:
-            h.update(fn.encode() + f.read())
+        if fn.startswith(("gemm_", "gemv_")) or fn == "sm100_ptx.cuh":
+            with open(os.path.join(cs, fn), "rb") as f:
+                h.update(fn.encode() + f.read())
     return h.hexdigest()[:16]
 
 

@@ -104,3 +104,22 @@ def test_default_workload_is_the_down_projection_decode():
     w = bench.WORKLOADS["down_8192x28672_m1"]
     assert w["layers"] == [(8192, 28672)] and w["M"] == 1 and w["fmt"] == "tq2"
     assert bench.TARGET_WORKLOADS == ("square_8192_m256", "llama7b_decode_m1")
+
+
+def test_recorded_traffic_is_of_the_present_gemm_kernels(tmp_path):
+    """The key follows the sources that the GEMM kernels come from, and no others."""
+    import os
+    import shutil
+    for w in ("down_8192x28672_m1", "llama7b_decode_m1", "square_8192_m256"):
+        assert bench.recorded_traffic("gemm", w) is not None
+    cs = tmp_path / "csrc"
+    shutil.copytree(os.path.join(bench.ROOT, "bit_mixed_precision_tri_b200", "csrc"), cs)
+    key = bench.kernel_source_hash()
+    assert bench.kernel_source_hash(str(cs)) == key
+    (cs / "paged.cu").write_text("// another\n")
+    assert bench.kernel_source_hash(str(cs)) == key
+    for name in ("gemv_i8.cu", "gemm_tc.cu", "sm100_ptx.cuh"):
+        text = (cs / name).read_text()
+        (cs / name).write_text(text + "\n")
+        assert bench.kernel_source_hash(str(cs)) != key
+        (cs / name).write_text(text)
