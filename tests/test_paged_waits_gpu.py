@@ -122,3 +122,44 @@ def test_check_option(polls):
     polls(-1)
     paged.qknorm_rope_append(*rows, check=True)
     assert torch.equal(paged.attention_decode(*args, check=True, **kw), want)
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing is looked up or set on first use that a capture forbids."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from bit_mixed_precision_tri_b200 import paged
+dev = "cuda:0"
+T = 2500
+qkv = torch.randn(T, 6 * 64, device=dev).half()
+k = torch.zeros(T // 8 + 1, 1, 8, 64, dtype=torch.float16, device=dev)
+v = torch.zeros_like(k)
+pos = torch.arange(T, dtype=torch.int32, device=dev)
+seq = torch.zeros_like(pos)
+table = torch.arange(T // 8 + 1, dtype=torch.int32, device=dev)[None]
+pools = torch.zeros(4, 1, 8, 64, dtype=torch.float16, device=dev)
+ids = torch.tensor([[0], [1]], dtype=torch.int32, device=dev)
+pools[0] = 5.0
+torch.cuda.synchronize()
+def calls():
+    cs = paged.rope_table(T, dev, rot=32)
+    q = paged.qknorm_rope_append(qkv, pos, None, None, cs, k, v, table, 4, seq=seq)
+    paged.qknorm_rope_append(qkv[:2], pos[:2], None, None, cs, k, v, table, 4, seq=seq[:2])
+    paged.copy_pages(pools, ids[0], ids[1])
+    return paged.attention_decode(q[-3:], k, v, table, pos[-3:], seq=seq[-3:])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = calls()
+g.replay()
+torch.cuda.synchronize()
+got = out.clone()
+assert bool((pools[1] == 5.0).all()) and bool((got != 0).any())
+assert torch.equal(calls(), got)
+print("captured first")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
