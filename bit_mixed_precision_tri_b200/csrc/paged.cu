@@ -3,9 +3,10 @@
 //
 //  * rope_table_scaled_kernel: (cos, sin) of p f_i, f_i = theta^(-2i/rot)
 //    under one of four scalings, all in float64, stored as float32 pairs.
-//  * paged_append_kernel: per row and head, y = x / sqrt(mean x^2 + eps) * g,
-//    the pairs of the first `rot` features turned by the row's angles, fp32,
-//    rounded once: fp16, or e4m3 of y / scale clamped to +-448.
+//  * paged_append_kernel (few rows) and paged_append_stream_kernel (many): per row
+//    and head, y = x / sqrt(mean x^2 + eps) * g, the pairs of the first `rot`
+//    features turned by the row's angles, fp32, rounded once: fp16, or e4m3 of
+//    y / scale clamped to +-448.
 //  * copy_pages_kernel: page src[i] of every pool to page dst[i].
 #include <cuda_fp8.h>
 
@@ -77,8 +78,7 @@ __device__ __forceinline__ uint32_t h2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight features of a head in fp32, as two fp32 pairs of four consecutive ones.
-// e4m3: value / scale (the IEEE quotient, so that the bytes are those of the
+// Four consecutive features of a head.  e4m3: value / scale (the IEEE quotient, so that the bytes are those of the
 // plain definition), clamped to +-448.
 template <bool FP8>
 __device__ __forceinline__ void store4(void* base, int64_t elem, const float* y, float scale) {

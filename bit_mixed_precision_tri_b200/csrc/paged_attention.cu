@@ -43,7 +43,6 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kMaxStages = 8;
 // A run of more tiles than this gives one-tile (row, head)s to single warps, which
 // take its blocks one after another and need no merge.  With / without, 8 heads x 60
 // positions in fp16: 300 rows (8 tiles a run) 18.5 / 22.4 us, 111 (3) 9.1 / 9.9, 74 (2)
@@ -82,8 +81,7 @@ struct Cfg {
   static constexpr int kQ = 8 * HG * kQRow;
   static constexpr int kMerge = HG * 2 * DH * 8 * 4;          // two warps' outputs of each group
   static constexpr int kRoom = (kCtasPerSm == 1 ? 224 : kCtasPerSm == 2 ? 113 : 75) * 1024 - kMerge - 2304;
-  static constexpr int kFit = kRoom / (2 * kKV + kQ);
-  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kStages = kRoom / (2 * kKV + kQ);       // 3 to 5
   static constexpr int kSmem = 1024 + kStages * (2 * kKV + kQ) + kMerge;
   static_assert(kStages >= 3, "a ring of three stages at least");
 };

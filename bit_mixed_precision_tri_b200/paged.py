@@ -177,6 +177,8 @@ def qknorm_rope_append(qkv: torch.Tensor, pos: torch.Tensor, gq, gk, cs: torch.T
 
 
 def attention_workspace_bytes(M: int, H: int, Hkv: int, head_dim: int = 128) -> int:
+    """What ``attention_decode`` needs of a workspace on the current device; 0 for
+    shapes that it refuses."""
     return int(_lib.lib().tri_paged_attention_workspace_bytes(M, H, Hkv, head_dim))
 
 
@@ -208,7 +210,7 @@ def attention_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: t
         if len(_WS_BYTES) > 4096:
             _WS_BYTES.clear()
         with torch.cuda.device(index):
-            nbytes = _WS_BYTES[key] = L.tri_paged_attention_workspace_bytes(M, H, heads, dh) or 256
+            nbytes = _WS_BYTES[key] = attention_workspace_bytes(M, H, heads, dh) or 256
     ws = workspace.get(nbytes) if workspace is not None else torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     if ws.get_device() != index:
         raise ValueError("the workspace must live on the tensors' device")
@@ -320,10 +322,8 @@ class PageBook:
         if need > self.seq_pages:
             raise CacheFull("the sequence outgrows its row of the page table")
         last = L // self.page_size                          # the page of the next position
-        partial = n > 0 and L % self.page_size and last < len(held)
-        if partial and held[last] < 0:
-            raise ValueError("the sequence's last page was dropped")
-        split = bool(partial) and self.count[held[last]] > 1
+        # a page that is not full is held: drop_front gives up full ones only
+        split = n > 0 and L % self.page_size > 0 and self.count[held[last]] > 1
         if max(0, need - len(held)) + split > len(self.free_pages):
             raise CacheFull("no free pages")
         src, dst = [], []
