@@ -10,6 +10,7 @@
 //  * copy_pages_kernel: page src[i] of every pool to page dst[i].
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <cfloat>
 #include <type_traits>
 
@@ -556,7 +557,7 @@ cudaError_t launch_paged_qknorm_rope(const __half* qkv, int64_t qkv_stride, cons
   const int smem = kAppendStages * p.stage_bytes;
   return pick([&](auto dh, auto e, auto il) -> cudaError_t {
     auto kernel = paged_append_stream_kernel<decltype(dh)::value, decltype(e)::value, decltype(il)::value>;
-    static bool ready[64] = {};
+    static std::atomic<bool> ready[64] = {};                    // host threads may call at once
     int dev = 0;
     cudaError_t r = cudaGetDevice(&dev);
     if (r != cudaSuccess) return r;

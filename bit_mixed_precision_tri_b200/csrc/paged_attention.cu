@@ -35,6 +35,8 @@
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "sm100_ptx.cuh"
 #include "tri_internal.cuh"
 
@@ -856,7 +858,7 @@ cudaError_t launch(Params p, const tri_paged_cache& c, void* ws, int sms, cudaSt
   }
   cudaError_t e = wait_status_word(&p.error);
   if (e != cudaSuccess) return e;
-  static bool ready[64] = {};
+  static std::atomic<bool> ready[64] = {};                      // host threads may call at once
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev]) {
