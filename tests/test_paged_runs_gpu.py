@@ -95,3 +95,40 @@ def test_runs_longer_than_the_ring(fp8, dh, H, Hkv, ps, M, longest):
     assert np.all(np.isfinite(got))
     assert np.all(np.abs(got - ref) <= tol), float(np.max(np.abs(got - ref) / tol))
     assert torch.equal(paged.attention_decode(*args, **kw), out)
+
+
+def test_as_many_rows_as_a_long_list():
+    """300000 rows of one sequence, a position more each row up to a page's end, then padding among them."""
+    M, dh, ps = 300000, 64, 256
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(1, 1, ps, dh, generator=g).half().to(DEV) for _ in range(2))
+    q = torch.randn(1, 1, dh, generator=g).half().to(DEV).expand(M, -1, -1).contiguous()
+    pos = (torch.arange(M, device=DEV) % 257 - 1).int()
+    table, seq = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.zeros(M, dtype=torch.int32, device=DEV)
+    out = paged.attention_decode(q, k, v, table, pos, seq=seq)
+    few = paged.attention_decode(q[:257], k, v, table, pos[:257], seq=seq[:257])
+    ref, tol = P.attention_rows_f64(q[:257].double().cpu().numpy(), k.double().cpu().numpy(), v.double().cpu().numpy(),
+                                    np.zeros((1, 1), np.int32), pos[:257].cpu().numpy(), np.zeros(257, np.int32), dh ** -0.5)
+    # every row within the bound; equal rows need not be equal bit for bit, since one that two runs share is summed in two parts
+    for got in (few, *out.split(257)):
+        n = len(got)
+        assert np.all(np.abs(got.double().cpu().numpy().reshape(n, 1, dh) - ref[:n]) <= tol[:n])
+
+
+@pytest.mark.parametrize("Hkv", [1, 3])
+def test_the_farthest_position_there_is(Hkv):
+    """A row at position 2^30 - 1: of its 2^27 pages the first, one in the middle and the last are present."""
+    dh, ps, n = 64, 8, 1 << 30
+    table = torch.full((1, n // ps), -1, dtype=torch.int32, device=DEV)
+    at = [0, (n // ps) // 2 + 5, n // ps - 1]
+    table[0, at] = torch.tensor([2, 0, 1], dtype=torch.int32, device=DEV)
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(3, Hkv, ps, dh, generator=g).half().to(DEV) for _ in range(2))
+    q = torch.randn(1, 2 * Hkv, dh, generator=g).half().to(DEV)
+    far = paged.attention_decode(q, k, v, table, torch.tensor([n - 1], dtype=torch.int32, device=DEV))
+    near = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV)
+    ref, tol = P.attention_rows_f64(q.double().cpu().numpy(), k.double().cpu().numpy(), v.double().cpu().numpy(),
+                                    near.cpu().numpy(), np.array([23]), np.array([0]), dh ** -0.5)
+    assert np.all(np.abs(far.double().cpu().numpy().reshape(ref.shape) - ref) <= tol)
+    clamped = paged.attention_decode(q, k, v, table, torch.tensor([2 ** 31 - 1], dtype=torch.int32, device=DEV))
+    assert torch.equal(clamped, far)
