@@ -278,8 +278,9 @@ paged_append_kernel(const AppendParams p) {
 // looks the rows up an item ahead (a lane per row) and bulk-copies them and
 // their angles into a ring of stages, so that every load's latency is behind
 // the items before it; eight warps turn and store.  Bound by memory: 16384 rows of 80
-// heads of 128 in fp16 117 us (5.8 TB/s, 89 % of a copy's rate; 122 without the
-// arithmetic), 5001 rows of 96 heads of 64 23-25 us (5.0-5.4 TB/s).
+// heads of 128 in fp16 123-125 us (5.5 TB/s, 84 % of a copy's rate, in graphs of calls
+// under the power cap; 117 before it sets in, 122 then without the arithmetic), 5001 rows
+// of 96 heads of 64 25.6 us (4.85 TB/s: 2501 items of two rows, 5.6 a CTA).
 // CTAs per SM of the few-row kernel up to which it is taken.  Few / many rows' kernel: 4 per SM (118 rows
 // of 80 heads) 3.0 / 5.1 us, 8 (592 of 20) 4.1 / 5.0, 16 (1184 of 20) 6.4 / 6.2, 20 (590 of 80) 7.4 / 8.2,
 // 32 (2400 of 20) 11.0 / 9.4, 40 (1180 of 80) 12.9 / 12.6

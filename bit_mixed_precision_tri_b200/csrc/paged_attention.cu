@@ -25,12 +25,16 @@
 //    elements become fp16 (exactly) in registers; the K scale joins the softmax
 //    scale, the V scale the output.
 //
-// Measured (B200, 64 query heads on 8 of 128 unless said): 16 rows x 4096 positions
-// in fp16 45.2 us (5.9 TB/s of K and V, 91 % of a copy's rate), 1 x 131072 87 us (94 %),
-// 100 ragged rows to 6000 in e4m3 96 us (93 %), 9 ragged rows to 20000 with 16 heads on
-// one 17.1 us (22 %: five tiles a CTA), 1 x 37 4.9 us, all in one graph.  A reference
-// that is raised only when it must be, instead of the exact maximum of every tile, took
-// 9 x 80000 with 16 heads on one in e4m3 from 58.6 to 53.2 us.
+// A row's tiles are counted from position 0: one in an absent page costs its turn in the
+// run, not its bytes.
+//
+// Measured (B200, 64 query heads on 8 of 128 unless said, graphs of calls, join included):
+// 16 rows x 4096 positions in fp16 47.4 us (5.7 TB/s of K and V, 87 % of a copy's rate),
+// 1 x 131072 88-89 us (92 %), 100 ragged rows to 6000 in e4m3 99-103 us (86 %), 9 ragged
+// rows to 20000 with 16 heads on one 18.0 us (20 %: five tiles a CTA), 9 x 80000 of those
+// 51-53 us (54 %), 1 x 37 4.9-5.2 us.  A reference that is raised only when it must be,
+// instead of the exact maximum of every tile, took 9 x 80000 from 58.6 to 53.2 us when it
+// came, a wait's first poll before its limit is looked at from 53.3 to 51.9.
 #include <cuda.h>
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
@@ -54,7 +58,7 @@ constexpr int kSoloRun = 1;
 // reach down to 2^-39 of the largest weight instead of 2^-25, below which a hundred
 // thousand small weights would vanish from the output but not from their sum.
 constexpr float kWeightShift = 14.f;
-constexpr float kWeightMost = 15.9f;         // log2 of the largest weight held in fp16 (65504)
+constexpr float kWeightMost = 15.9f;         // log2: above it a weight would near fp16's largest, 65504
 constexpr float kNothing = -3e38f;           // the reference before any position: below every score
 constexpr unsigned kProducerCode = 51, kConsumerCode = 52, kDrainCode = 53;
 
@@ -63,7 +67,7 @@ template <int DH, bool FP8, int HG>
 struct Cfg {
   static constexpr int kWarps = 4 * HG;                       // consumer warps
   static constexpr int kThreads = 32 * (kWarps + 2);          // and two producer warps, of K and of V
-  // Two CTAs per SM; one where 320 threads of 164 registers leave no other choice, three
+  // Two CTAs per SM; one where 320 threads of 162-165 registers leave no other choice, three
   // where a position is 64 bytes and registers and stages fit.  (16 heads on one of 64,
   // 9 x 80000: two CTAs at 96 registers 36.3 us, one at 142 39.8, in fp16; 35.1 and 41.3
   // in e4m3.  12 heads of 64, 37 x 6000 in e4m3: three CTAs 63.7 us, two 70.3.)

@@ -838,3 +838,28 @@ def test_block_on_pages_has_angles_for_every_position_of_its_cache():
         outs.append(blk.step(x, _t([40], torch.int32), seq=_t([s], torch.int32)).clone())
         assert blk.cs.shape[0] == 64
     assert torch.equal(*outs) and torch.all(torch.isfinite(outs[0]))
+
+
+def test_cache_forked_before_its_room_is_written():
+    """Room for 12 positions of which 5 are written at the fork: each continues with its own keys and values."""
+    c = paged.PagedCache(6, 2, 2, 3, DEV, layers=2, page_size=8, head_dim=64)
+    a = c.new(12)
+    cs, g = paged.rope_table(24, DEV, rot=16), torch.Generator().manual_seed(4)
+
+    def write(s, lo, hi):
+        rows = torch.randn(hi - lo, 6 * 64, generator=g).half().to(DEV)
+        for i in range(2):
+            k, v, _, _ = c.layer(i)
+            paged.qknorm_rope_append(rows * (i + 1), torch.arange(lo, hi, dtype=torch.int32, device=DEV), None, None, cs,
+                                     k, v, c.table, 2, seq=torch.full((hi - lo,), s, dtype=torch.int32, device=DEV))
+        return rows[:, 256:].view(-1, 2, 64)
+
+    head = write(a, 0, 5)
+    b = c.fork(a, written=5)
+    assert c.free_pages == 2                                  # the half-written page and the empty one are b's own
+    want = {s: torch.cat([head, write(s, 5, 12)]) for s in (a, b)}
+    for s in (a, b):
+        for i in range(2):
+            v = c.layer(i)[1]
+            got = torch.stack([v[int(c.table[s, p // 8]), :, p % 8] for p in range(12)])
+            assert torch.equal(got, want[s] * (i + 1))
